@@ -63,6 +63,8 @@ typedef enum {
   ARL2_ERR_STATE = 6        /* call out of order, such as a query before the feature maps are set */
 } arl2_status;
 
+typedef enum { ARL2_BF16 = 0, ARL2_FP16 = 1, ARL2_FP32 = 2 } arl2_dtype;
+
 /* Create a layer for B independent streams of H heads, T tokens per frame and head
  * dims d_k = d_v. Allocates the fp32 state S (two buffers, which alternate per commit),
  * a bf16 copy of S, the feature-map copies, scratch and staging. S starts at 0 and the
@@ -287,6 +289,63 @@ int arl2_kvcache_frames(const arl2_kvcache* c);
 arl2_status arl2_kvcache_get_status(arl2_kvcache* c);
 size_t arl2_kvcache_memory_bytes(const arl2_kvcache* c);
 void arl2_kvcache_destroy(arl2_kvcache* c);
+
+/* ---- Gated linear recurrence, for training and serving ----------------------------------
+ * The simplest member of the family the layer's recurrent branch belongs to: a state per
+ * channel with a forget gate, over the tokens t of each sequence b,
+ *   h_t = a_t h_{t-1} + x_t,     h_{-1} = h0
+ * and its backward pass, for dh the gradient of h and dfinal that of the last state,
+ *   lam_t = dh_t + a_{t+1} lam_{t+1},   lam_{T-1} = dh_{T-1} + dfinal,
+ *   dx_t = lam_t,   da_t = lam_t h_{t-1},   dh0 = a_0 lam_0.
+ * The gates a are given as values (any real number: 0 forgets, 1 keeps), either one per
+ * channel and token, or one per head and token in the layout of arl2_frame_gates' alpha. With
+ * T = 1 the forward call is the serving step: h0 in, final_state out.
+ *
+ * Shapes: x, h, dh, dx [B, T, C] of type dtype (bf16, fp16 or fp32). heads = 0: gates
+ * [B, T, C] of type dtype or fp32. heads > 0: gates fp32 [B, heads, T], each for the d =
+ * C / heads channels of its head, d in {32, 64, 128}; da is the sum over those channels.
+ * h0, dfinal, final_state, dh0: fp32 [B, C] contiguous; each may be NULL (0 as an input, not
+ * written as an output), and final_state may be h0. lens: int32 [B] in device memory, or NULL:
+ * the tokens of sequence b are t < lens[b] (clamped to [0, T]); final_state is the state
+ * after the last of them, h, dx and da are 0 behind it, and what x, a, h and dh hold there is
+ * not used.
+ * Strides are in elements, channels adjacent: x_stride and the like are (batch, token),
+ * a_stride (batch, token, head), its last unused with heads = 0. Inputs may have stride 0;
+ * an output's elements must not share memory. da is contiguous. Pointers are aligned to
+ * their elements; with heads > 0, x, h, dh and dx to 4 elements, with strides of a multiple
+ * of 4. Outputs must not overlap inputs, except that h may be x and dx may be dh (same
+ * strides).
+ * All arithmetic is fp32; h, dx and da are rounded once. da uses the stored (rounded) h.
+ * The calls take no context, allocate nothing and hold nothing between calls: calls on
+ * different streams are independent. The current device must hold every buffer. */
+typedef struct {
+  int B, T, C, heads;
+  arl2_dtype dtype, gate_dtype;
+  const int* lens;
+} arl2_scan_shape;
+typedef struct {
+  arl2_scan_shape shape;
+  const void* x;
+  const void* a;
+  const float* h0;
+  void* h;
+  float* final_state;
+  int64_t x_stride[2], a_stride[3], h_stride[2];
+} arl2_scan_fwd;
+typedef struct {
+  arl2_scan_shape shape;
+  const void* dh;
+  const void* a;
+  const void* h;
+  const float* h0;
+  const float* dfinal;
+  void* dx;
+  void* da;
+  float* dh0;
+  int64_t dh_stride[2], a_stride[3], h_stride[2], dx_stride[2];
+} arl2_scan_bwd;
+arl2_status arl2_scan_forward(const arl2_scan_fwd* f, arl2_stream stream);
+arl2_status arl2_scan_backward(const arl2_scan_bwd* f, arl2_stream stream);
 
 #ifdef __cplusplus
 }

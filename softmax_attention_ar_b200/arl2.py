@@ -23,6 +23,7 @@ STATUS_NAMES = {
     4: "ARL2_ERR_CUDA", 5: "ARL2_ERR_TIMEOUT", 6: "ARL2_ERR_STATE",
 }
 
+_I64 = ctypes.c_int64
 _P, _I, _S, _U64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
 # name -> (restype, argtypes); the names and order follow include/arl2.h.
 SIGNATURES = {
@@ -59,7 +60,26 @@ SIGNATURES = {
     "arl2_kvcache_get_status": (_S, [_P]),
     "arl2_kvcache_memory_bytes": (_SZ, [_P]),
     "arl2_kvcache_destroy": (None, [_P]),
+    "arl2_scan_forward": (_S, [_P, _P]),
+    "arl2_scan_backward": (_S, [_P, _P]),
 }
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # arl2_dtype
+
+
+class _ScanShape(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("C", _I), ("heads", _I), ("dtype", _I), ("gate_dtype", _I), ("lens", _P)]
+
+
+class _ScanFwd(ctypes.Structure):
+    _fields_ = [("shape", _ScanShape), ("x", _P), ("a", _P), ("h0", _P), ("h", _P), ("final_state", _P),
+                ("x_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2)]
+
+
+class _ScanBwd(ctypes.Structure):
+    _fields_ = [("shape", _ScanShape), ("dh", _P), ("a", _P), ("h", _P), ("h0", _P), ("dfinal", _P), ("dx", _P),
+                ("da", _P), ("dh0", _P), ("dh_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2),
+                ("dx_stride", _I64 * 2)]
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -395,3 +415,149 @@ class KVCacheBaseline:
     @property
     def memory_bytes(self) -> int:
         return self._lib.arl2_kvcache_memory_bytes(self._c)
+
+
+# ------------------------------------------------- training operators: the gated recurrence
+class _OnStream:
+    """The device and stream of a call whose tensors may live on a device that is not current.
+
+    With stream=None the call runs on the current stream of the tensors' device, as torch's
+    own operators do. With a stream given, outputs are allocated for that stream and the inputs
+    are recorded on it, so that the allocator does not hand their memory on while the call
+    still reads it.
+    """
+    __slots__ = ("ctx", "ptr")
+
+    def __init__(self, device, stream, inputs):
+        self.ctx = None
+        if stream is None:
+            if device.index != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(device)
+            self.ptr = torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"stream: on {stream.device}, the tensors on {device}")
+        self.ptr = stream.cuda_stream
+        self.ctx = torch.cuda.stream(stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _want(t, name, device, dtypes, shape, contiguous=False):
+    """Check one tensor argument (None passes)."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dtype not in dtypes or t.shape != shape:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if not contiguous and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: its last dimension must be adjacent in memory")
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.device
+
+
+def _scan_args(x, a, lens, name):
+    device = _cuda_device(x, name)
+    if x.dim() != 3 or x.dtype not in DTYPES:
+        raise ValueError(f"{name}: expected bf16, fp16 or fp32 [B, T, C], got {x.dtype} {tuple(x.shape)}")
+    B, T, C = x.shape
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise TypeError("a must be a torch.Tensor [B, T, C] or [B, heads, T]")
+    # A gate tensor of x's shape is per channel; one whose last dimension is T is per head.
+    heads = 0 if a.shape == x.shape else a.shape[1]
+    if heads:
+        if a.device != device or a.dtype != torch.float32 or a.shape != (B, heads, T) or heads < 1 or C % heads:
+            raise ValueError(f"a: expected gates {(B, T, C)}, or fp32 [B, heads, T] with heads dividing {C}, got "
+                             f"{a.dtype} {tuple(a.shape)}")
+        sa = a.stride()
+        a_stride = (sa[0], sa[2], sa[1])
+    else:
+        _want(a, "a", device, (x.dtype, torch.float32), x.shape)
+        a_stride = (a.stride(0), a.stride(1), 0)
+    _want(lens, "lens", device, (torch.int32,), (B,), True)
+    return device, _ScanShape(B, T, C, heads, DTYPES[x.dtype], DTYPES[a.dtype], _ptr(lens)), a_stride
+
+
+def scan_forward(x, a, h0=None, lens=None, out=None, final=None, stream=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + x_t along dim 1; returns (h, final state).
+
+    x bf16, fp16 or fp32 [B, T, C]; a the gates, [B, T, C] of x's type or fp32, or one per head
+    and token, fp32 [B, heads, T] with C / heads in {32, 64, 128} (the layout of
+    ``ARL2Layer.gates``); where both shapes fit, per channel is meant. h0 fp32 [B, C], 0 if
+    None. lens int32 [B]: behind lens[b] h is 0, and the final state is that of the last token
+    inside. With T = 1 this is the serving step. out may be x, final may be h0.
+    """
+    device, shape, a_stride = _scan_args(x, a, lens, "x")
+    B, T, C = x.shape
+    _want(x, "x", device, (x.dtype,), x.shape)
+    _want(h0, "h0", device, (torch.float32,), (B, C), True)
+    _want(out, "out", device, (x.dtype,), x.shape)
+    _want(final, "final", device, (torch.float32,), (B, C), True)
+    with _OnStream(device, stream, (x, a, h0, lens, out, final)) as st:
+        if out is None:
+            out = torch.empty((B, T, C), dtype=x.dtype, device=device)
+        if final is None:
+            final = torch.empty((B, C), dtype=torch.float32, device=device)
+        f = _ScanFwd(shape, x.data_ptr(), a.data_ptr(), _ptr(h0), out.data_ptr(), final.data_ptr(), x.stride()[:2],
+                     a_stride, out.stride()[:2])
+        _check(load_library().arl2_scan_forward(ctypes.byref(f), st), "arl2_scan_forward")
+    return out, final
+
+
+def scan_backward(dh, a, h, h0=None, dfinal=None, lens=None, dx=None, da=None, dh0=None, stream=None):
+    """The backward pass of scan_forward; returns (dx, da, dh0).
+
+    dh the gradient of h, [B, T, C] of h's type; a, h0, lens as in the forward call and h its
+    output; dfinal fp32 [B, C] the gradient of the final state (0 if None). dx has dh's type;
+    da the type and shape of a, contiguous; dh0 fp32 [B, C]. dx may be dh.
+    """
+    device, shape, a_stride = _scan_args(dh, a, lens, "dh")
+    B, T, C = dh.shape
+    _want(dh, "dh", device, (dh.dtype,), dh.shape)
+    if h is None:
+        raise TypeError("h must be a torch.Tensor")
+    _want(h, "h", device, (dh.dtype,), dh.shape)
+    _want(h0, "h0", device, (torch.float32,), (B, C), True)
+    _want(dfinal, "dfinal", device, (torch.float32,), (B, C), True)
+    _want(dx, "dx", device, (dh.dtype,), dh.shape)
+    _want(da, "da", device, (a.dtype,), a.shape, True)
+    _want(dh0, "dh0", device, (torch.float32,), (B, C), True)
+    with _OnStream(device, stream, (dh, a, h, h0, dfinal, lens, dx, da, dh0)) as st:
+        if dx is None:
+            dx = torch.empty((B, T, C), dtype=dh.dtype, device=device)
+        if da is None:
+            da = torch.empty(a.shape, dtype=a.dtype, device=device)
+        if dh0 is None:
+            dh0 = torch.empty((B, C), dtype=torch.float32, device=device)
+        f = _ScanBwd(shape, dh.data_ptr(), a.data_ptr(), h.data_ptr(), _ptr(h0), _ptr(dfinal), dx.data_ptr(),
+                     da.data_ptr(), dh0.data_ptr(), dh.stride()[:2], a_stride, h.stride()[:2], dx.stride()[:2])
+        _check(load_library().arl2_scan_backward(ctypes.byref(f), st), "arl2_scan_backward")
+    return dx, da, dh0
