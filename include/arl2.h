@@ -316,8 +316,12 @@ void arl2_kvcache_destroy(arl2_kvcache* c);
  * of 4. Outputs must not overlap inputs, except that h may be x and dx may be dh (same
  * strides).
  * All arithmetic is fp32; h, dx and da are rounded once. da uses the stored (rounded) h.
- * The calls take no context, allocate nothing and hold nothing between calls: calls on
- * different streams are independent. The current device must hold every buffer. */
+ * The calls take no context, allocate nothing and hold nothing between calls. A sequence of
+ * more than a few hundred tokens is cut into chunks whose gate products and partial sums pass
+ * through workspace: device memory of arl2_scan_workspace_bytes(&shape) bytes (0: none is
+ * needed), 16-byte aligned, whose content means nothing before and after a call. Calls that may
+ * overlap on the GPU need workspaces of their own. The current device must hold every
+ * buffer. */
 typedef struct {
   int B, T, C, heads;
   arl2_dtype dtype, gate_dtype;
@@ -330,6 +334,7 @@ typedef struct {
   const float* h0;
   void* h;
   float* final_state;
+  void* workspace;
   int64_t x_stride[2], a_stride[3], h_stride[2];
 } arl2_scan_fwd;
 typedef struct {
@@ -342,8 +347,10 @@ typedef struct {
   void* dx;
   void* da;
   float* dh0;
+  void* workspace;
   int64_t dh_stride[2], a_stride[3], h_stride[2], dx_stride[2];
 } arl2_scan_bwd;
+size_t arl2_scan_workspace_bytes(const arl2_scan_shape* shape);
 arl2_status arl2_scan_forward(const arl2_scan_fwd* f, arl2_stream stream);
 arl2_status arl2_scan_backward(const arl2_scan_bwd* f, arl2_stream stream);
 

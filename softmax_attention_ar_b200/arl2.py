@@ -60,6 +60,7 @@ SIGNATURES = {
     "arl2_kvcache_get_status": (_S, [_P]),
     "arl2_kvcache_memory_bytes": (_SZ, [_P]),
     "arl2_kvcache_destroy": (None, [_P]),
+    "arl2_scan_workspace_bytes": (_SZ, [_P]),
     "arl2_scan_forward": (_S, [_P, _P]),
     "arl2_scan_backward": (_S, [_P, _P]),
 }
@@ -73,12 +74,12 @@ class _ScanShape(ctypes.Structure):
 
 class _ScanFwd(ctypes.Structure):
     _fields_ = [("shape", _ScanShape), ("x", _P), ("a", _P), ("h0", _P), ("h", _P), ("final_state", _P),
-                ("x_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2)]
+                ("workspace", _P), ("x_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2)]
 
 
 class _ScanBwd(ctypes.Structure):
     _fields_ = [("shape", _ScanShape), ("dh", _P), ("a", _P), ("h", _P), ("h0", _P), ("dfinal", _P), ("dx", _P),
-                ("da", _P), ("dh0", _P), ("dh_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2),
+                ("da", _P), ("dh0", _P), ("workspace", _P), ("dh_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2),
                 ("dx_stride", _I64 * 2)]
 
 _lib: Optional[ctypes.CDLL] = None
@@ -506,6 +507,11 @@ def _scan_args(x, a, lens, name):
     return device, _ScanShape(B, T, C, heads, DTYPES[x.dtype], DTYPES[a.dtype], _ptr(lens)), a_stride
 
 
+def _scan_workspace(shape, device):
+    n = load_library().arl2_scan_workspace_bytes(ctypes.byref(shape))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
 def scan_forward(x, a, h0=None, lens=None, out=None, final=None, stream=None):
     """The gated linear recurrence h_t = a_t h_{t-1} + x_t along dim 1; returns (h, final state).
 
@@ -526,8 +532,9 @@ def scan_forward(x, a, h0=None, lens=None, out=None, final=None, stream=None):
             out = torch.empty((B, T, C), dtype=x.dtype, device=device)
         if final is None:
             final = torch.empty((B, C), dtype=torch.float32, device=device)
-        f = _ScanFwd(shape, x.data_ptr(), a.data_ptr(), _ptr(h0), out.data_ptr(), final.data_ptr(), x.stride()[:2],
-                     a_stride, out.stride()[:2])
+        ws = _scan_workspace(shape, device)
+        f = _ScanFwd(shape, x.data_ptr(), a.data_ptr(), _ptr(h0), out.data_ptr(), final.data_ptr(), _ptr(ws),
+                     x.stride()[:2], a_stride, out.stride()[:2])
         _check(load_library().arl2_scan_forward(ctypes.byref(f), st), "arl2_scan_forward")
     return out, final
 
@@ -557,7 +564,9 @@ def scan_backward(dh, a, h, h0=None, dfinal=None, lens=None, dx=None, da=None, d
             da = torch.empty(a.shape, dtype=a.dtype, device=device)
         if dh0 is None:
             dh0 = torch.empty((B, C), dtype=torch.float32, device=device)
+        ws = _scan_workspace(shape, device)
         f = _ScanBwd(shape, dh.data_ptr(), a.data_ptr(), h.data_ptr(), _ptr(h0), _ptr(dfinal), dx.data_ptr(),
-                     da.data_ptr(), dh0.data_ptr(), dh.stride()[:2], a_stride, h.stride()[:2], dx.stride()[:2])
+                     da.data_ptr(), dh0.data_ptr(), _ptr(ws), dh.stride()[:2], a_stride, h.stride()[:2],
+                     dx.stride()[:2])
         _check(load_library().arl2_scan_backward(ctypes.byref(f), st), "arl2_scan_backward")
     return dx, da, dh0

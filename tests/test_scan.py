@@ -2,9 +2,9 @@
 the GPU against a token-by-token loop in 64 bits.
 
 Error bounds. The kernels work in fp32: every product and sum on the way from an input to an
-output rounds by at most u = 2^-24 relative. A token's gate enters one product, and each
-super-chunk of at least 128 tokens adds at most 24 compositions, so an input passes through
-fewer than 2 T + 80 roundings; the error of h_t is below (2 T + 80) u times the same recurrence
+output rounds by at most u = 2^-24 relative. A token's gate enters one product of its slice
+and one step of the second scan, and slices (of 8 tokens or more) and chunks are composed once
+each, so an input passes through fewer than 2 T + 80 roundings; the error of h_t is below (2 T + 80) u times the same recurrence
 over absolute values, and a stored value is off by half a step of its type on top
 (eps / 2 relative, and half the smallest subnormal of fp16).
 """
@@ -139,14 +139,14 @@ def test_gates_per_head(B, T, heads, d, dtype):
 @on_gpu
 @pytest.mark.parametrize("heads,C", [(0, 96), (0, 61), (2, 64)])
 def test_lengths(heads, C):
-    # Full, empty, one token, one short of full, inside a super-chunk; NaN behind each.
+    # Full, empty, one token, one short of full, inside a slice; NaN behind each.
     check(5, 300, C, heads, "bf16", "fp32", lens=[300, 0, 1, 299, 129])
     check(3, 2, C, heads, "fp32", "fp32", lens=[0, 2, 1], state=False)
 
 
 @on_gpu
-def test_many_channel_groups_take_one_cta_each():
-    # Enough (batch, channel group) pairs that no cluster is used, over several super-chunks.
+def test_many_channel_groups():
+    # Enough (batch, channel group) pairs that slices are long.
     check(96, 300, 520, 0, "bf16", "fp32", lens=[300 - 3 * b for b in range(96)])
 
 
@@ -333,8 +333,8 @@ def test_c_entry_refuses_without_a_gpu():
     p = 1 << 20   # an aligned address; never dereferenced by the argument checks
 
     def fwd(B=2, T=8, C=64, heads=0, dtype=2, gate=2, x=p, a=p, h=p, h0=None, xs=(512, 64), as_=(512, 64, 0),
-            hs=(512, 64)):
-        f = arl2._ScanFwd(arl2._ScanShape(B, T, C, heads, dtype, gate, None), x, a, h0, h, None, xs, as_, hs)
+            hs=(512, 64), ws=None):
+        f = arl2._ScanFwd(arl2._ScanShape(B, T, C, heads, dtype, gate, None), x, a, h0, h, None, ws, xs, as_, hs)
         return lib.arl2_scan_forward(ctypes.byref(f), None)
 
     bad, unsup = arl2.ARL2_ERR_INVALID_ARG, arl2.ARL2_ERR_UNSUPPORTED
@@ -349,13 +349,15 @@ def test_c_entry_refuses_without_a_gpu():
     assert fwd(heads=2, xs=(512, 66)) == bad          # rows not aligned to 4 elements
     assert fwd(xs=(-512, 64)) == bad
     assert fwd(hs=(0, 64)) == bad and fwd(hs=(512, 32)) == bad and fwd(hs=(256, 64)) == bad
+    assert lib.arl2_scan_workspace_bytes(None) == 0
+    assert fwd(B=1, T=5000, xs=(0, 64), as_=(0, 64, 0), hs=(0, 64)) == bad   # needs a workspace
     sh = arl2._ScanShape(2, 8, 64, 0, 2, 2, None)
     s2, s3 = (512, 64), (512, 64, 0)
     for hole in range(5):
         q = [p] * 5
         q[hole] = None
         dh, a, h, dx, da = q
-        f = arl2._ScanBwd(sh, dh, a, h, None, None, dx, da, None, s2, s3, s2, s2)
+        f = arl2._ScanBwd(sh, dh, a, h, None, None, dx, da, None, None, s2, s3, s2, s2)
         assert lib.arl2_scan_backward(ctypes.byref(f), None) == bad
-    f = arl2._ScanBwd(sh, p, p, p, None, None, p, p, None, s2, s3, s2, (512, 0))
+    f = arl2._ScanBwd(sh, p, p, p, None, None, p, p, None, None, s2, s3, s2, (512, 0))
     assert lib.arl2_scan_backward(ctypes.byref(f), None) == bad
