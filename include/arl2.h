@@ -290,6 +290,69 @@ arl2_status arl2_kvcache_get_status(arl2_kvcache* c);
 size_t arl2_kvcache_memory_bytes(const arl2_kvcache* c);
 void arl2_kvcache_destroy(arl2_kvcache* c);
 
+/* ---- Softmax attention for training -----------------------------------------------------
+ * The layer's intra-frame branch, and the full attention over frames that it is trained from,
+ * with what their gradients need: a forward call that keeps its row statistics and a backward
+ * call that recomputes the probabilities from them. Per batch b and query head h, with the key
+ * head h / (H / H_kv) (H a multiple of H_kv),
+ *   forward:   o = softmax(scale q k^T) v,   lse_i = log sum_j exp(scale q_i . k_j)
+ *   backward:  P = exp(scale q k^T - lse),  delta_i = do_i . o_i,  dS = P (do v^T - delta),
+ *              dv = P^T do,  dk = scale dS^T q,  dq = scale dS k
+ * (dk and dv summed over the query heads that share a key head).
+ * Key j is visible to query i if i < q_len[b], j < k_len[b] and, with frame_len > 0,
+ *   j < (floor((i + q_start) / frame_len) + 1) * frame_len:
+ * a query sees its own frame and the frames before it (frame_len = 1: causal), q_start being the
+ * place of query 0 among the keys. A row that sees nothing has o = 0, lse = -inf and dq = 0;
+ * dk and dv are 0 where nothing sees the key. Rows of q, o and do behind q_len, and of k and v
+ * behind k_len, may hold anything: they reach no result, and the rows of o, dq, dk and dv
+ * there are 0, those of lse -inf.
+ * q, o, do, dq: [B, Tq, H, d]; k, v, dk, dv: [B, Tk, H_kv, d], of the context's type (bf16 or
+ * fp16), d in {32, 64, 128}, given as a pointer and strides in elements (batch, token, head),
+ * elements of a head adjacent: pointers 16-byte aligned, strides positive multiples of 8 (any
+ * for dimensions of size 1), so q, k and v may lie in one projection's output. An output's
+ * elements must not share memory, and outputs must not overlap inputs. lse: fp32
+ * [B, H, Tq] contiguous. q_len, k_len: int32 [B] in device memory (clamped to [0, Tq], [0, Tk]),
+ * or NULL for full lengths. scale: finite and positive, or 0 for 1 / sqrt(d).
+ * P and dS are rounded to the type for the tensor cores; statistics, sums and gradients are
+ * fp32 until they are stored, rounded once. Results do not depend on timing. */
+typedef struct arl2_attn arl2_attn; /* opaque; owned by the library */
+typedef struct {
+  void* ptr;
+  int64_t stride[3];
+} arl2_tensor;
+typedef struct {
+  int Tq, Tk;
+  const int* q_len;
+  const int* k_len;
+  int frame_len, q_start;
+  float scale;
+} arl2_attn_shape;
+typedef struct {
+  arl2_attn_shape shape;
+  arl2_tensor q, k, v, o;
+  float* lse;
+} arl2_attn_fwd;
+typedef struct {
+  arl2_attn_shape shape;
+  arl2_tensor q, k, v, o, d_o, dq, dk, dv;
+  const float* lse;
+} arl2_attn_bwd;
+
+/* Create a context for B sequences of H query and H_kv key heads, up to max_Tq queries and
+ * max_Tk keys (at most 2^28), on the current device. It allocates the scratch of both calls
+ * (about 40 MB at d = 128, plus 8 bytes per query row and head) and no call allocates more.
+ * Calls with smaller Tq and Tk are served by the same context. The device must be current in
+ * every call. Calls on one context, replays of captured ones included, share its scratch: they
+ * must be ordered, normally by one stream. */
+arl2_status arl2_attn_create(int B, int H, int H_kv, int max_Tq, int max_Tk, int d, arl2_dtype dtype,
+                             arl2_attn** out);
+arl2_status arl2_attn_forward(arl2_attn* ctx, const arl2_attn_fwd* f, arl2_stream stream);
+arl2_status arl2_attn_backward(arl2_attn* ctx, const arl2_attn_bwd* f, arl2_stream stream);
+/* As arl2_get_status, arl2_memory_bytes and arl2_destroy. */
+arl2_status arl2_attn_get_status(arl2_attn* ctx);
+size_t arl2_attn_memory_bytes(const arl2_attn* ctx);
+void arl2_attn_destroy(arl2_attn* ctx);
+
 /* ---- Gated linear recurrence, for training and serving ----------------------------------
  * The simplest member of the family the layer's recurrent branch belongs to: a state per
  * channel with a forget gate, over the tokens t of each sequence b,

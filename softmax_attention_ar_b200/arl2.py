@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -60,10 +61,23 @@ SIGNATURES = {
     "arl2_kvcache_get_status": (_S, [_P]),
     "arl2_kvcache_memory_bytes": (_SZ, [_P]),
     "arl2_kvcache_destroy": (None, [_P]),
+    "arl2_attn_create": (_S, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_P)]),
+    "arl2_attn_forward": (_S, [_P, _P, _P]),
+    "arl2_attn_backward": (_S, [_P, _P, _P]),
+    "arl2_attn_get_status": (_S, [_P]),
+    "arl2_attn_memory_bytes": (_SZ, [_P]),
+    "arl2_attn_destroy": (None, [_P]),
     "arl2_scan_workspace_bytes": (_SZ, [_P]),
     "arl2_scan_forward": (_S, [_P, _P]),
     "arl2_scan_backward": (_S, [_P, _P]),
 }
+
+# The argument structs of the training operators, as byte layouts (include/arl2.h): packing one is
+# several times faster than filling a ctypes.Structure, which small calls would notice.
+_ATTN_SHAPE = "iiPPiif4x"
+_TENSOR = "P3q"
+_ATTN_FWD = struct.Struct(_ATTN_SHAPE + 4 * _TENSOR + "P")
+_ATTN_BWD = struct.Struct(_ATTN_SHAPE + 8 * _TENSOR + "P")
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # arl2_dtype
 
@@ -570,3 +584,144 @@ def scan_backward(dh, a, h, h0=None, dfinal=None, lens=None, dx=None, da=None, d
                      dx.stride()[:2])
         _check(load_library().arl2_scan_backward(ctypes.byref(f), st), "arl2_scan_backward")
     return dx, da, dh0
+
+
+# ---------------------------------------------------- training operators: softmax attention
+class SoftmaxAttention:
+    """Softmax attention with its row statistics and its backward pass (arl2_attn_* in arl2.h).
+
+    For B sequences of H query heads over H_kv key heads (H a multiple of H_kv), head dim d in
+    {32, 64, 128}, bf16 or fp16, up to max_Tq queries and max_Tk keys. ``forward`` returns
+    (o, lse); ``backward`` takes them with do and returns (dq, dk, dv). q, o, do, dq are
+    [B, Tq, H, d], k, v, dk, dv [B, Tk, H_kv, d], lse fp32 [B, H, Tq]; inputs may be strided
+    views (16-byte aligned, strides multiples of 8), such as slices of one packed projection.
+
+    Mask: key j is visible to query i if i < q_len[b], j < k_len[b] (int32 [B], None: all) and,
+    with frame_len > 0, j < (floor((i + q_start) / frame_len) + 1) * frame_len: its own frame
+    and the ones before it (frame_len = 1: causal), q_start being the place of query 0 among
+    the keys. Rows that see nothing give o = 0, lse = -inf. scale defaults to 1 / sqrt(d).
+
+    The scratch belongs to the object: calls on one object, and replays of graphs that captured
+    them, must be ordered, normally by one stream.
+    """
+
+    def __init__(self, H: int, max_Tq: int, max_Tk: int, d: int, B: int = 1, H_kv: Optional[int] = None,
+                 dtype: torch.dtype = torch.bfloat16, device=None):
+        self.H, self.d, self.B, self.H_kv, self.dtype = H, d, B, H if H_kv is None else H_kv, dtype
+        self.max_Tq, self.max_Tk = max_Tq, max_Tk
+        self._c = None
+        if dtype not in DTYPES:
+            raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {dtype}")
+        self._lib = load_library()
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"device: expected a CUDA device, got {self.device}")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        out = _P()
+        with torch.cuda.device(self.device):
+            _check(self._lib.arl2_attn_create(B, H, self.H_kv, max_Tq, max_Tk, d, DTYPES[dtype], ctypes.byref(out)),
+                   "arl2_attn_create")
+        self._c = out
+
+    def close(self) -> None:
+        if self._c is not None:
+            with torch.cuda.device(self.device):
+                self._lib.arl2_attn_destroy(self._c)
+            self._c = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _lengths(self, q, k):
+        for t, name in ((q, "q"), (k, "k")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dim() != 4:
+                raise ValueError(f"{name}: expected [B, T, heads, d], got {tuple(t.shape)}")
+        if self._c is None:
+            raise Arl2Error(ARL2_ERR_INVALID_ARG, "a closed SoftmaxAttention")
+        return q.shape[1], k.shape[1]
+
+    def _check(self, t, name, shape):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != self.device or t.dtype != self.dtype or t.shape != shape or t.stride(3) != 1:
+            raise ValueError(f"{name}: expected {self.dtype} {tuple(shape)} on {self.device}, its last dimension "
+                             f"adjacent in memory; got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+    def _check_lse(self, lse, Tq):
+        _want(lse, "lse", self.device, (torch.float32,), (self.B, self.H, Tq), True)
+
+    def _shape(self, Tq, Tk, q_len, k_len, frame_len, q_start, scale):
+        _want(q_len, "q_len", self.device, (torch.int32,), (self.B,), True)
+        _want(k_len, "k_len", self.device, (torch.int32,), (self.B,), True)
+        for v, name in ((frame_len, "frame_len"), (q_start, "q_start")):
+            if not -(1 << 31) <= v < 1 << 31:
+                raise ValueError(f"{name}: {v} does not fit an int")
+        if scale is not None and not 0.0 < scale < float("inf"):
+            raise ValueError(f"scale: expected a positive number, got {scale}")
+        return (Tq, Tk, _ptr(q_len) or 0, _ptr(k_len) or 0, frame_len, q_start, 0.0 if scale is None else scale)
+
+    def forward(self, q, k, v, out=None, lse=None, q_len=None, k_len=None, frame_len: int = 0, q_start: int = 0,
+                scale: Optional[float] = None, stream=None):
+        """o = softmax(scale q k^T + mask) v and the rows' lse; returns (o, lse)."""
+        Tq, Tk = self._lengths(q, k)
+        qs, ks = (self.B, Tq, self.H, self.d), (self.B, Tk, self.H_kv, self.d)
+        self._check(q, "q", qs)
+        self._check(k, "k", ks)
+        self._check(v, "v", ks)
+        shape = self._shape(Tq, Tk, q_len, k_len, frame_len, q_start, scale)
+        with _OnStream(self.device, stream, (q, k, v, out, lse, q_len, k_len)) as st:
+            if out is None:
+                out = torch.empty(qs, dtype=self.dtype, device=self.device)
+            else:
+                self._check(out, "out", qs)
+            if lse is None:
+                lse = torch.empty((self.B, self.H, Tq), dtype=torch.float32, device=self.device)
+            else:
+                self._check_lse(lse, Tq)
+            f = _ATTN_FWD.pack(*shape, q.data_ptr(), *q.stride()[:3], k.data_ptr(), *k.stride()[:3], v.data_ptr(),
+                               *v.stride()[:3], out.data_ptr(), *out.stride()[:3], lse.data_ptr())
+            _check(self._lib.arl2_attn_forward(self._c, f, st), "arl2_attn_forward")
+        return out, lse
+
+    def backward(self, do, q, k, v, o, lse, dq=None, dk=None, dv=None, q_len=None, k_len=None, frame_len: int = 0,
+                 q_start: int = 0, scale: Optional[float] = None, stream=None):
+        """The gradients of q, k and v from do, with o and lse of the forward call and its mask
+        and scale; returns (dq, dk, dv)."""
+        Tq, Tk = self._lengths(q, k)
+        qs, ks = (self.B, Tq, self.H, self.d), (self.B, Tk, self.H_kv, self.d)
+        for t, name, s in ((do, "do", qs), (q, "q", qs), (k, "k", ks), (v, "v", ks), (o, "o", qs)):
+            self._check(t, name, s)
+        if lse is None:
+            raise TypeError("lse must be a torch.Tensor")
+        self._check_lse(lse, Tq)
+        shape = self._shape(Tq, Tk, q_len, k_len, frame_len, q_start, scale)
+        with _OnStream(self.device, stream, (do, q, k, v, o, lse, dq, dk, dv, q_len, k_len)) as st:
+            outs = []
+            for t, name, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks)):
+                if t is None:
+                    t = torch.empty(s, dtype=self.dtype, device=self.device)
+                else:
+                    self._check(t, name, s)
+                outs.append(t)
+            fields = []
+            for t in (q, k, v, o, do, *outs):
+                fields.append(t.data_ptr())
+                fields += t.stride()[:3]
+            f = _ATTN_BWD.pack(*shape, *fields, lse.data_ptr())
+            _check(self._lib.arl2_attn_backward(self._c, f, st), "arl2_attn_backward")
+        return tuple(outs)
+
+    def status(self) -> int:
+        """Synchronise and return (and clear) the device status (ARL2_OK, ARL2_ERR_TIMEOUT, ...)."""
+        with torch.cuda.device(self.device):
+            return self._lib.arl2_attn_get_status(self._c)
+
+    @property
+    def memory_bytes(self) -> int:
+        return self._lib.arl2_attn_memory_bytes(self._c)

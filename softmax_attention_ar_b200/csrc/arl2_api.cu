@@ -174,13 +174,21 @@ constexpr unsigned long long kDefaultTimeoutNs = 1000000000ull;
 
 }  // namespace
 
-// Entry points for other translation units of the library (the allocation-free commit).
+// Entry points for other translation units of the library (the allocation-free commit, the
+// recurrence and the training attention).
 namespace arl2 {
 int prepare_device(int* dev, int* sms) { return static_cast<int>(check_device(dev, sms)); }
 bool encode_act_map(CUtensorMap* m, const void* ptr, int B, int L, int H, int d) {
   return make_act_map(m, ptr, B, L, H, d);
 }
 bool encode_mat_map(CUtensorMap* m, const void* ptr, int n, int d) { return make_mat_map(m, ptr, n, d); }
+bool encode_strided_map(CUtensorMap* m, const void* ptr, int B, int T, int heads, int d, long long sb, long long st,
+                        long long sh) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t str[3] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2, (cuuint64_t)sb * 2};
+  const cuuint32_t box[4] = {64, 1, 128, 1};
+  return make_map(m, ptr, 4, dims, str, box);
+}
 }  // namespace arl2
 
 struct arl2_ctx {

@@ -1,0 +1,333 @@
+// Shared parts of the training attention kernels (arl2_attn_fwd.cu, arl2_attn_bwd.cu): the
+// mask, the split of the work over the CTAs, tile copies and MMA blocks.
+//
+// Mask. Key j is visible to query i of batch b if i < q_len[b], j < k_len[b] and, with
+// frame_len F > 0, j < (floor((i + q_start) / F) + 1) F. The visible keys of a row are thus a
+// prefix: row i sees the keys below limit(i), which never falls as i grows. A key's visible
+// rows are a suffix of the rows inside q_len, from first_row(j) on.
+//
+// Split. A tile (of query rows, or of keys in the dk/dv kernel) has as many units as it has
+// visible (query tile, key tile) pairs, at least one (an empty tile still writes its zeros).
+// The units of all tiles, in order, are cut into equal contiguous ranges, one per CTA, so that
+// every SM gets the same work whatever the lengths and masks are. A tile whose units fall to
+// several CTAs is a sum of partial records in the workspace: the CTA that arrives last (an
+// atomic counter, which it sets back to 0) adds them in the order of the CTAs, so the result
+// does not depend on who it is. No CTA waits for another.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "arl2_device.cuh"
+
+namespace arl2 {
+
+struct AttnMask {
+  const int* q_len;   // [B] or null
+  const int* k_len;   // [B] or null
+  int Tq, Tk;
+  int F;              // frame_len, 0: none
+  int q_start;
+};
+
+namespace {
+
+__device__ __forceinline__ int q_length(const AttnMask& m, int b) {
+  return m.q_len ? min(max(m.q_len[b], 0), m.Tq) : m.Tq;
+}
+__device__ __forceinline__ int k_length(const AttnMask& m, int b) {
+  return m.k_len ? min(max(m.k_len[b], 0), m.Tk) : m.Tk;
+}
+__device__ __forceinline__ int floor_div(int x, int y) {
+  const int q = x / y;
+  return q * y > x ? q - 1 : q;
+}
+// Keys visible to row i (kl: the batch's key length).
+__device__ __forceinline__ int key_limit(const AttnMask& m, int i, int kl) {
+  if (m.F == 0) return kl;
+  const long long lim = (static_cast<long long>(floor_div(i + m.q_start, m.F)) + 1) * m.F;
+  return static_cast<int>(lim < 0 ? 0 : lim < kl ? lim : kl);
+}
+// First row that sees key j (may be negative or past the last row).
+__device__ __forceinline__ int first_row(const AttnMask& m, int j) {
+  return m.F == 0 ? -(1 << 30) : j / m.F * m.F - m.q_start;
+}
+
+// Units of a tile. Rows: tile i is query rows [i kRowsPerTile, ...), its units the key tiles that
+// its last row sees. Keys: tile j is keys [128 j, ...), its units the (query head of the group,
+// query tile) pairs that see its first key.
+template <int kRowsPerTile>
+struct RowTiles {
+  static __device__ int count(const AttnMask& m) { return (m.Tq + kRowsPerTile - 1) / kRowsPerTile; }
+  static __device__ int valid(const AttnMask& m, int ql, int) { return (ql + kRowsPerTile - 1) / kRowsPerTile; }
+  static __device__ int units(const AttnMask& m, int i, int ql, int kl, int) {
+    if (i * kRowsPerTile >= ql) return 0;
+    return (key_limit(m, min(ql, (i + 1) * kRowsPerTile) - 1, kl) + kRows - 1) / kRows;
+  }
+};
+struct KeyTiles {
+  static __device__ int count(const AttnMask& m) { return (m.Tk + kRows - 1) / kRows; }
+  static __device__ int valid(const AttnMask& m, int, int kl) { return (kl + kRows - 1) / kRows; }
+  static __device__ int first_tile(const AttnMask& m, int j) { return max(0, first_row(m, j * kRows)) / kRows; }
+  static __device__ int units(const AttnMask& m, int j, int ql, int kl, int group) {
+    if (j * kRows >= kl) return 0;
+    return max(0, (ql + kRows - 1) / kRows - first_tile(m, j)) * group;
+  }
+};
+
+// Where a CTA's range starts; computed by one warp, read by every role.
+struct Split {
+  long long u0, u1, total;
+  int ctas;                  // CTAs that have a range
+  int b, h, tile, off;       // of unit u0
+};
+
+// Sum over a batch's tiles of the units of one head (at least one each), by one warp.
+template <typename Tiles>
+__device__ long long head_units(const AttnMask& m, int b, int group) {
+  const int ql = q_length(m, b), kl = k_length(m, b), n = Tiles::count(m);
+  if (m.F == 0) {   // every valid tile has the same
+    const int v = Tiles::valid(m, ql, kl);
+    return static_cast<long long>(v) * max(1, Tiles::units(m, 0, ql, kl, group)) + (n - v);
+  }
+  long long s = 0;
+  for (int i = threadIdx.x & 31; i < n; i += 32) s += max(1, Tiles::units(m, i, ql, kl, group));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+template <typename Tiles>
+__device__ void make_split(const AttnMask& m, int B, int heads, int group, int min_units, Split* out) {
+  const int lane = threadIdx.x & 31;
+  const bool ragged = m.q_len || m.k_len;
+  long long total = 0, per_head = 0;
+  if (!ragged) {
+    per_head = head_units<Tiles>(m, 0, group);
+    total = per_head * heads * B;
+  } else {
+    for (int b = 0; b < B; ++b) total += head_units<Tiles>(m, b, group) * heads;
+  }
+  // Few units per CTA cost more in merging than they save: at least min_units each, unless the
+  // tiles alone are more.
+  const long long tiles = static_cast<long long>(Tiles::count(m)) * heads * B;
+  long long ctas = max(tiles, total / min_units);
+  ctas = max(1ll, min(min(ctas, total), static_cast<long long>(gridDim.x)));
+  const int c = blockIdx.x;
+  Split s{};
+  s.ctas = static_cast<int>(ctas);
+  s.total = total;
+  if (c < ctas) {
+    s.u0 = c * total / ctas;
+    s.u1 = (c + 1) * total / ctas;
+    long long r = s.u0;
+    if (!ragged) {
+      const long long per_batch = per_head * heads;
+      s.b = static_cast<int>(r / per_batch);
+      r -= s.b * per_batch;
+    } else {
+      for (; s.b < B; ++s.b) {
+        per_head = head_units<Tiles>(m, s.b, group);
+        if (r < per_head * heads) break;
+        r -= per_head * heads;
+      }
+    }
+    s.h = static_cast<int>(r / per_head);
+    r -= s.h * per_head;
+    const int ql = q_length(m, s.b), kl = k_length(m, s.b), n = Tiles::count(m);
+    if (m.F == 0) {
+      const int v = Tiles::valid(m, ql, kl), w = max(1, Tiles::units(m, 0, ql, kl, group));
+      if (r < static_cast<long long>(v) * w) {
+        s.tile = static_cast<int>(r / w);
+        s.off = static_cast<int>(r - static_cast<long long>(s.tile) * w);
+      } else {
+        s.tile = v + static_cast<int>(r - static_cast<long long>(v) * w);
+      }
+    } else {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int w = i0 + lane < n ? max(1, Tiles::units(m, i0 + lane, ql, kl, group)) : 0;
+        int inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const int sum = __shfl_sync(0xffffffffu, inc, 31);
+        if (r < sum) {
+          const unsigned found = __ballot_sync(0xffffffffu, r < inc);
+          const int l = __ffs(found) - 1;
+          s.tile = i0 + l;
+          s.off = static_cast<int>(r) - (__shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, w, l));
+          break;
+        }
+        r -= sum;
+      }
+    }
+  }
+  if (lane == 0) *out = s;
+}
+
+// One segment: units [kb, ke) of a tile.
+struct Seg {
+  int b, h, tile, kb, ke;
+  int units;         // the tile's units (0: nothing is visible, one unit stands for writing zeros)
+  int ql, kl;
+  long long first;   // global index of the tile's first unit
+  bool whole, range_start;
+};
+template <typename Tiles>
+struct Walk {
+  const AttnMask& m;
+  int heads, group, ntiles;
+  long long u, u0, u1;
+  int b, h, tile, off;
+  __device__ Walk(const AttnMask& mask, const Split& s, int heads_, int group_)
+      : m(mask), heads(heads_), group(group_), ntiles(Tiles::count(mask)), u(s.u0), u0(s.u0), u1(s.u1), b(s.b), h(s.h),
+        tile(s.tile), off(s.off) {}
+  __device__ bool next(Seg& g) {
+    if (u >= u1) return false;
+    g.b = b;
+    g.h = h;
+    g.tile = tile;
+    g.ql = q_length(m, b);
+    g.kl = k_length(m, b);
+    g.units = Tiles::units(m, tile, g.ql, g.kl, group);
+    const int w = max(1, g.units);
+    g.kb = off;
+    g.ke = static_cast<int>(min(static_cast<long long>(w), off + (u1 - u)));
+    g.first = u - off;
+    g.whole = g.kb == 0 && g.ke == w;
+    g.range_start = u == u0;
+    u += g.ke - g.kb;
+    off = 0;
+    if (++tile == ntiles) {
+      tile = 0;
+      if (++h == heads) {
+        h = 0;
+        ++b;
+      }
+    }
+    return true;
+  }
+};
+// The CTA that holds unit u, and the record slot of a CTA's segment of the tile whose first unit
+// is `first`: a CTA has at most two segments of tiles it shares, the first and the last of its
+// range.
+__device__ __forceinline__ int unit_owner(const Split& s, long long u) {
+  return static_cast<int>(((u + 1) * s.ctas - 1) / s.total);
+}
+__device__ __forceinline__ int record_slot(const Split& s, int c, long long first) {
+  return 2 * c + (c * s.total / s.ctas >= first ? 0 : 1);
+}
+
+// ------------------------------------------------------------------ element types
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kHalf) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
+}
+// kind::f16 instruction descriptor for fp16 or bf16 operands (both of one type).
+template <bool kHalf>
+__host__ __device__ constexpr uint32_t attn_idesc(int N, bool a_mn, bool b_mn) {
+  return kHalf ? idesc_bf16(128, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10)) : idesc_bf16(128, N, a_mn, b_mn);
+}
+
+// ------------------------------------------------------------------ tiles
+template <int D>
+struct TileOf {
+  static constexpr int kPanels = D > 64 ? 2 : 1;
+  static constexpr uint32_t kBytes = kPanels * kPanelBytes;
+  static constexpr int kSteps = D / 16;   // K-steps of a contraction over the head dim
+};
+// Copy 128 rows of one head to a swizzled tile (the caller has announced kBytes to the barrier).
+// Rows behind the tensor's end and columns behind d read as zero.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int row, int b) {
+#pragma unroll
+  for (int p = 0; p < TileOf<D>::kPanels; ++p) tma_load_4d(dst + p * kPanelBytes, map, bar, 64 * p, head, row, b);
+}
+// Zero rows [r0, 128) of a tile, by one warp: what stands behind a length must not reach a
+// contraction over rows (0 times a NaN is a NaN).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int r0) {
+  const int n = (kRows - r0) * 8;
+#pragma unroll
+  for (int p = 0; p < TileOf<D>::kPanels; ++p)
+    for (int i = threadIdx.x & 31; i < n; i += 32) st_shared_v4(tile + p * kPanelBytes + r0 * 128 + i * 16, 0, 0, 0, 0);
+}
+// A tile whose rows from r0 on (r0 < 128: some) are to read as zero: copied on the side barrier,
+// patched, then handed over on `full` as a plain arrival. Otherwise copied straight to `full`.
+template <int D>
+__device__ __forceinline__ bool load_clean(uint32_t dst, const CUtensorMap* map, uint32_t full, uint32_t side,
+                                           uint32_t& side_phase, int head, int row, int b, int r0, bool lead,
+                                           const Guard& g) {
+  if (r0 >= kRows) {
+    if (lead) {
+      mbar_expect_tx(full, TileOf<D>::kBytes);
+      load_tile<D>(dst, map, full, head, row, b);
+    }
+    return true;
+  }
+  if (lead) {
+    mbar_expect_tx(side, TileOf<D>::kBytes);
+    load_tile<D>(dst, map, side, head, row, b);
+  }
+  __syncwarp();
+  // The copy lands by itself: the wait must not end before it, whatever other roles do.
+  if (!mbar_wait_drain(side, side_phase & 1)) {
+    raise_timeout(g);
+    return false;
+  }
+  ++side_phase;
+  zero_rows<D>(dst, r0);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lead) mbar_arrive(full);
+  return true;
+}
+
+// ------------------------------------------------------------------ MMA blocks (issuing lane)
+// D[tmem] = A B^T over the head dim, both operands K-major tiles.
+template <int D>
+__device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, uint32_t idesc) {
+  if constexpr (D == 128) {
+    mma8_ss<false, false>(d_tmem, desc_kmajor(a_tile, 0), desc_kmajor(b_tile, 0), idesc, 0u);
+  } else {
+    const uint64_t a0 = desc_kmajor(a_tile, 0), b0 = desc_kmajor(b_tile, 0);
+#pragma unroll
+    for (int s = 0; s < TileOf<D>::kSteps; ++s) mma_bf16(d_tmem, a0 + kmajor_step16(s), b0 + kmajor_step16(s), idesc, s > 0);
+  }
+}
+// D[tmem] (+)= P B over 128 rows: P packed in TMEM (columns a + 8 s, the second half of the
+// steps kSplit columns further than that), B a tile of 128 rows (MN-major).
+template <int kSplit>
+__device__ __forceinline__ void mma_over_rows(uint32_t d_tmem, uint32_t a, uint32_t b_tile, uint32_t idesc,
+                                              uint32_t acc) {
+  constexpr uint32_t col[8] = {0, 8, 16, 24, 32 + kSplit, 40 + kSplit, 48 + kSplit, 56 + kSplit};
+  mma8_ts(d_tmem, a, col, desc_mnmajor(b_tile, 0), idesc, acc);
+}
+
+// Registers per thread of the calling warpgroup (all four of its warps): give some back, or take
+// them. The sum over the block must not exceed what it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Rendezvous of a group of warps with a bounded wait (no hang if a warp gave up).
+__device__ __forceinline__ bool warps_sync(uint32_t bar, uint32_t& phase, const Guard& g) {
+  warp_arrive(bar);
+  const bool ok = mbar_wait_warp(bar, phase & 1, g);
+  ++phase;
+  return ok;
+}
+
+}  // namespace
+}  // namespace arl2

@@ -1,0 +1,783 @@
+// Backward pass of softmax attention with the probabilities recomputed (arl2_attn_backward):
+//     P = exp(scale q k^T - lse),   delta_i = sum_c do_ic o_ic,   dP = do v^T,   dS = P (dP - delta)
+//     dv = P^T do,   dk = scale dS^T q,   dq = scale dS k
+// over the visible pairs (arl2_attn.cuh). lse comes from the forward call, so P needs no second
+// pass over the keys.
+//
+// The tensor cores bound it. Three launches:
+//   - arl2_attn_prep_kernel: delta, and lse in log2 units (+inf where a row sees nothing or lies
+//     behind its length: P is then 0 without further tests), padded to whole 128-row tiles;
+//   - arl2_attn_dkv_kernel: a tile is 128 keys of one key head; it runs over the query tiles of
+//     every query head that shares the head, so the heads' sum stays in the accumulators;
+//   - arl2_attn_dq_kernel: a tile is 128 query rows of one head; it runs over the key tiles.
+// S and dP are computed in both, 7 products a tile pair instead of the 5 of a single pass. In
+// return no dq leaves the SM before it is complete: a single pass would add 64 KiB of fp32 per
+// tile pair to memory, with atomics whose order changes the result or an ordering that stalls,
+// and dS would pass through shared memory. Here P and dS go back to TMEM, in place over the
+// scores they came from, and feed the next product as its A operand; shared memory holds only
+// what TMA brought.
+//
+// Roles (384 threads, one CTA per SM): warp 0 copies, warp 1 issues every MMA, warps 4-11 turn
+// scores into P and dS: thread = TMEM lane = row of the tile, warps 4-7 columns 0-63, 8-11 columns
+// 64-127, each in two packed halves (32 columns in place of 64 fp32 ones, at columns 0 and 64).
+// P and dS are rounded to 16 bits for the tensor cores; sums, statistics and gradients are fp32.
+#include <algorithm>
+
+#include "arl2_attn_kernels.h"
+
+namespace arl2 {
+namespace {
+
+constexpr int kBwdThreads = 384;
+constexpr uint32_t kBCtl = 512;   // barriers, split, flags
+struct Ctl {                      // after the barriers, at ctl + 320
+  Split split;
+  uint32_t tmem;
+  int abort;
+  int last[2];
+};
+static_assert(sizeof(Ctl) <= 192, "control block");
+template <int D>
+constexpr uint32_t bwd_smem() {
+  return 7 * TileOf<D>::kBytes + 2 * 1024 + kBCtl;
+}
+static_assert(bwd_smem<128>() <= 232448, "shared memory per CTA");
+
+template <bool kHalf>
+__device__ __forceinline__ void store32(uint16_t* dst, const float (&x)[32]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 8)
+    *reinterpret_cast<uint4*>(dst + c) =
+        make_uint4(pack2<kHalf>(x[c], x[c + 1]), pack2<kHalf>(x[c + 2], x[c + 3]), pack2<kHalf>(x[c + 4], x[c + 5]),
+                   pack2<kHalf>(x[c + 6], x[c + 7]));
+}
+
+// Write kCols accumulator columns of this thread's row to an output, times scale: straight when
+// the segment is the whole tile; otherwise as one of the tile's records, which the group of 4
+// warps that arrives last adds up in the order of the CTAs. rec_off: this group's place in a
+// record, [kCols / 4][128] float4. Returns false when a wait ran out.
+template <int kCols, bool kHalf>
+__device__ bool write_rows(const AttnArgs& a, const Split& sp, const Seg& sg, uint32_t acc, int r, bool inside,
+                           bool zero, uint16_t* dst, float scale, size_t rec_floats, size_t rec_off,
+                           unsigned int* counter, uint32_t group_bar, uint32_t& group_phase, uint32_t empty_bar,
+                           int* last_flag, const Guard& g) {
+  float* rec = a.records + record_slot(sp, static_cast<int>(blockIdx.x), sg.first) * rec_floats + rec_off;
+#pragma unroll 1
+  for (int k = 0; k < kCols; k += 32) {
+    uint32_t x[32];
+    tmem_ld32_wait(acc + k, x);
+    if (sg.whole) {
+      float y[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) y[e] = zero ? 0.f : __uint_as_float(x[e]) * scale;
+      if (inside) store32<kHalf>(dst + k, y);
+    } else {
+      float4* ro = reinterpret_cast<float4*>(rec);
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        ro[(k + e) / 4 * kRows + r] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                 __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+    }
+  }
+  tc_fence_before();
+  warp_arrive(empty_bar);
+  if (sg.whole) return true;
+  __threadfence();
+  if (!warps_sync(group_bar, group_phase, g)) return false;
+  const int c0 = unit_owner(sp, sg.first), c1 = unit_owner(sp, sg.first + sg.units - 1);
+  if (r == 0) {
+    const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c1 - c0);
+    if (last) *counter = 0;
+    *static_cast<volatile int*>(last_flag) = last;
+  }
+  if (!warps_sync(group_bar, group_phase, g)) return false;
+  if (!*static_cast<volatile int*>(last_flag)) return true;
+  __threadfence();
+#pragma unroll 1
+  for (int k = 0; k < kCols; k += 32) {
+    float y[32] = {};
+    for (int j = c0; j <= c1; ++j) {
+      const float4* oj =
+          reinterpret_cast<const float4*>(a.records + record_slot(sp, j, sg.first) * rec_floats + rec_off);
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 v = __ldcg(oj + (k + e) / 4 * kRows + r);
+        y[e] += v.x;
+        y[e + 1] += v.y;
+        y[e + 2] += v.z;
+        y[e + 3] += v.w;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) y[e] = zero ? 0.f : y[e] * scale;
+    if (inside) store32<kHalf>(dst + k, y);
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ prep
+template <bool kHalf>
+__global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_constant__ AttnPrepArgs a) {
+  const int lanes = a.d / 8;                        // lanes per row, 16 bytes each
+  const int Tpad = (a.Tq + kRows - 1) / kRows * kRows;
+  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / lanes;   // (b, t, h), h fastest
+  const int part = threadIdx.x % lanes;
+  if (row >= static_cast<long long>(a.B) * Tpad * a.H) return;   // whole rows leave together
+  const int h = static_cast<int>(row % a.H);
+  const long long bt = row / a.H;
+  const int t = static_cast<int>(bt % Tpad), b = static_cast<int>(bt / Tpad);
+  const int ql = a.q_len ? min(max(a.q_len[b], 0), a.Tq) : a.Tq;
+  float s = 0.f, l = INFINITY;
+  if (t < ql) {
+    const uint4 ov = *reinterpret_cast<const uint4*>(a.o + b * a.o_sb + t * a.o_st + h * a.o_sh + part * 8);
+    const uint4 gv = *reinterpret_cast<const uint4*>(a.g + b * a.g_sb + t * a.g_st + h * a.g_sh + part * 8);
+    const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, gw[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 x, y;
+      if constexpr (kHalf) {
+        x = __half22float2(*reinterpret_cast<const __half2*>(&ow[i]));
+        y = __half22float2(*reinterpret_cast<const __half2*>(&gw[i]));
+      } else {
+        x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ow[i]));
+        y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[i]));
+      }
+      s = fmaf(x.x, y.x, s);
+      s = fmaf(x.y, y.y, s);
+    }
+    const float lse = a.lse[(static_cast<size_t>(b) * a.H + h) * a.Tq + t];
+    l = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+  }
+  const int lane = threadIdx.x & 31;
+  const unsigned mask = ((1u << lanes) - 1) << (lane / lanes * lanes);   // the row's lanes
+  for (int m = lanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(mask, s, m);
+  if (part == 0) {
+    float* out = a.stats + (static_cast<size_t>(b) * a.H + h) * 2 * Tpad + t;
+    out[0] = l;
+    out[Tpad] = s;
+  }
+}
+
+// ------------------------------------------------------------------ dk, dv
+enum : int {
+  kKKVFull = 0,
+  kKKVEmpty,
+  kKQFull,                // + stage (3)
+  kKQEmpty = kKQFull + 3,
+  kKGFull = kKQEmpty + 3,   // + stage (2): do
+  kKGEmpty = kKGFull + 2,
+  kKTFull = kKGEmpty + 2,   // + stage (2): statistics
+  kKTEmpty = kKTFull + 2,   // 8 warps
+  kKSFull = kKTEmpty + 2,
+  kKPReady,               // 8 warps
+  kKDFull,
+  kKDReady,               // 8 warps
+  kKAccFull,
+  kKAccEmpty,             // 8 warps
+  kKGroup,                // + group (2), 4 warps
+  kKSide = kKGroup + 2,
+  kKFinal,                // the MMA warp's commit and 8 warps
+  kKBars
+};
+static_assert(kKBars * 8 <= 320, "control block");
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    arl2_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                         const __grid_constant__ AttnArgs a) {
+  using TO = TileOf<D>;
+  extern __shared__ __align__(1024) uint8_t attn_smem[];
+  const uint32_t base = smem_u32(attn_smem);
+  const uint32_t k_tile = base, v_tile = base + TO::kBytes, q_ring = base + 2 * TO::kBytes,
+                 g_ring = base + 5 * TO::kBytes, t_ring = base + 7 * TO::kBytes, ctl = t_ring + 2048;
+  uint8_t* gctl = attn_smem + 7 * TO::kBytes + 2048;
+  auto bar = [&](int i) { return ctl + 8u * i; };
+  Ctl* shared = reinterpret_cast<Ctl*>(gctl + 320);
+  const int warp = threadIdx.x >> 5;
+  const Guard g{&shared->abort, a.err, a.timeout_ns};
+  const int group = a.H / a.Hkv;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKBars; ++i) {
+      const bool by8 = i == kKTEmpty || i == kKTEmpty + 1 || i == kKPReady || i == kKDReady || i == kKAccEmpty;
+      mbar_init(bar(i), by8 ? 8 : i == kKGroup || i == kKGroup + 1 ? 4 : i == kKFinal ? 9 : 1);
+    }
+    shared->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    if (elect_one()) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      prefetch_tmap(&tm_g);
+    }
+    __syncwarp();
+    make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, 4, &shared->split);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = shared->tmem;
+  const uint32_t c_s = tmem, c_dp = tmem + 128, c_dv = tmem + 256, c_dk = tmem + 384;
+
+  // Registers move from the copy and MMA warps to the others: 128 threads x 88 + 256 x 200 = 62464
+  // of the block's 384 x 168.
+  if (warp == 0) {
+    regs_dec<88>();
+    const Split sp = shared->split;
+    Walk<KeyTiles> walk(a.mask, sp, a.Hkv, group);
+    Seg sg;
+    const bool lead = elect_one();
+    const int Tpad = (a.mask.Tq + kRows - 1) / kRows * kRows;
+    uint32_t ns = 0, nq = 0, ng = 0, nt = 0, side_phase = 0;   // copies made
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      if (sg.units == 0) continue;
+      if (ns > 0 && !mbar_wait_warp(bar(kKKVEmpty), (ns - 1) & 1, g)) break;
+      if (lead) {
+        mbar_expect_tx(bar(kKKVFull), 2 * TO::kBytes);
+        load_tile<D>(k_tile, &tm_k, bar(kKKVFull), sg.h, sg.tile * kRows, sg.b);
+        load_tile<D>(v_tile, &tm_v, bar(kKKVFull), sg.h, sg.tile * kRows, sg.b);
+      }
+      ++ns;
+      const int per_head = sg.units / group, first = KeyTiles::first_tile(a.mask, sg.tile);
+      int hd = sg.h * group + sg.kb / per_head, i = first + sg.kb % per_head;
+      for (int u = sg.kb; u < sg.ke; ++u) {
+        const int r0 = sg.ql < a.mask.Tq ? sg.ql - i * kRows : kRows;   // rows behind the length read as zero
+        ok = nq < 3 || mbar_wait_warp(bar(kKQEmpty + nq % 3), (nq / 3 - 1) & 1, g);
+        if (!ok) break;
+        ok = load_clean<D>(q_ring + nq % 3 * TO::kBytes, &tm_q, bar(kKQFull + nq % 3), bar(kKSide), side_phase, hd,
+                           i * kRows, sg.b, r0, lead, g);
+        ++nq;
+        if (!ok) break;
+        ok = nt < 2 || mbar_wait_warp(bar(kKTEmpty + nt % 2), (nt / 2 - 1) & 1, g);
+        if (!ok) break;
+        if (lead) {
+          const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + hd) * 2 * Tpad + i * kRows;
+          mbar_expect_tx(bar(kKTFull + nt % 2), 1024);
+          bulk_load(t_ring + nt % 2 * 1024, st, 512, bar(kKTFull + nt % 2));
+          bulk_load(t_ring + nt % 2 * 1024 + 512, st + Tpad, 512, bar(kKTFull + nt % 2));
+        }
+        ++nt;
+        ok = ng < 2 || mbar_wait_warp(bar(kKGEmpty + ng % 2), (ng / 2 - 1) & 1, g);
+        if (!ok) break;
+        ok = load_clean<D>(g_ring + ng % 2 * TO::kBytes, &tm_g, bar(kKGFull + ng % 2), bar(kKSide), side_phase, hd,
+                           i * kRows, sg.b, r0, lead, g);
+        ++ng;
+        if (!ok) break;
+        if (++i == first + per_head) {
+          i = first;
+          ++hd;
+        }
+      }
+    }
+    __syncwarp();
+    // Every copy issued lands before the CTA may exit.
+    if (ns > 0) mbar_wait_drain(bar(kKKVFull), (ns - 1) & 1);
+    for (uint32_t s = 0; s < 3; ++s)
+      if (nq > s) mbar_wait_drain(bar(kKQFull + s), ((nq - s + 2) / 3 - 1) & 1);
+    for (uint32_t s = 0; s < 2; ++s) {
+      if (ng > s) mbar_wait_drain(bar(kKGFull + s), ((ng - s + 1) / 2 - 1) & 1);
+      if (nt > s) mbar_wait_drain(bar(kKTFull + s), ((nt - s + 1) / 2 - 1) & 1);
+    }
+  } else if (warp == 1) {
+    regs_dec<88>();
+    const Split sp = shared->split;
+    Walk<KeyTiles> walk(a.mask, sp, a.Hkv, group);
+    Seg sg;
+    const bool lead = elect_one();
+    constexpr uint32_t id_s = attn_idesc<kHalf>(128, false, false), id_d = attn_idesc<kHalf>(D, false, true);
+    uint32_t ns = 0, n = 0;   // segments and units begun
+    bool ok = true;
+    auto q_full = [&](uint32_t i) { return mbar_wait_warp(bar(kKQFull + i % 3), (i / 3) & 1, g); };
+    auto g_full = [&](uint32_t i) { return mbar_wait_warp(bar(kKGFull + i % 2), (i / 2) & 1, g); };
+    auto q_at = [&](uint32_t i) { return q_ring + i % 3 * TO::kBytes; };
+    auto g_at = [&](uint32_t i) { return g_ring + i % 2 * TO::kBytes; };
+    while (ok && walk.next(sg)) {
+      if (sg.units == 0) continue;
+      ok = mbar_wait_warp(bar(kKKVFull), ns & 1, g) && q_full(n);
+      if (!ok) break;
+      tc_fence_after();
+      if (lead) {
+        mma_over_d<D>(c_s, k_tile, q_at(n), id_s);
+        mma_commit(bar(kKSFull));
+      }
+      __syncwarp();
+      ok = g_full(n);
+      if (!ok) break;
+      tc_fence_after();
+      if (lead) {
+        mma_over_d<D>(c_dp, v_tile, g_at(n), id_s);
+        mma_commit(bar(kKDFull));
+      }
+      __syncwarp();
+      for (int u = sg.kb; u < sg.ke; ++u, ++n) {
+        const bool more = u + 1 < sg.ke;
+        const uint32_t acc = u > sg.kb;
+        ok = mbar_wait_warp(bar(kKPReady), n & 1, g);
+        if (ok && !acc && ns > 0) ok = mbar_wait_warp(bar(kKAccEmpty), (ns - 1) & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {
+          mma_over_rows<32>(c_dv, c_s, g_at(n), id_d, acc);
+          mma_commit(bar(kKGEmpty + n % 2));
+        }
+        __syncwarp();
+        if (more) {
+          ok = q_full(n + 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+            mma_over_d<D>(c_s, k_tile, q_at(n + 1), id_s);
+            mma_commit(bar(kKSFull));
+          }
+          __syncwarp();
+        }
+        ok = mbar_wait_warp(bar(kKDReady), n & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {
+          mma_over_rows<32>(c_dk, c_dp, q_at(n), id_d, acc);
+          mma_commit(bar(kKQEmpty + n % 3));
+        }
+        __syncwarp();
+        if (more) {
+          ok = g_full(n + 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+            mma_over_d<D>(c_dp, v_tile, g_at(n + 1), id_s);
+            mma_commit(bar(kKDFull));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (lead) {
+        mma_commit(bar(kKAccFull));
+        mma_commit(bar(kKKVEmpty));
+      }
+      __syncwarp();
+      ++ns;
+    }
+    __syncwarp();
+    if (lead) mma_commit(bar(kKFinal));
+    __syncwarp();
+  } else if (warp < 4) {
+    regs_dec<88>();
+  } else {
+    regs_inc<200>();
+    const Split sp = shared->split;
+    Walk<KeyTiles> walk(a.mask, sp, a.Hkv, group);
+    Seg sg;
+    const int wg = (warp >> 2) - 1;                            // columns 64 wg ..; dv (0) or dk (1) at the end
+    const int r = (warp & 3) * 32 + (threadIdx.x & 31);        // key row == TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
+    const uint32_t s_col = c_s + lanes + 64u * wg, dp_col = c_dp + lanes + 64u * wg;
+    const float to_log2 = a.scale * 1.4426950408889634f;
+    uint32_t n = 0, ns = 0, group_phase = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int j = sg.tile * kRows + r;
+      const AttnOut& out = wg ? a.dk : a.dv;
+      uint16_t* dst = out.ptr + sg.b * out.sb + j * out.st + sg.h * out.sh;
+      const bool inside = j < a.mask.Tk;
+      if (sg.units == 0) {
+        float z[32] = {};
+        for (int k = 0; k < D; k += 32)
+          if (inside) store32<kHalf>(dst + k, z);
+        continue;
+      }
+      const int per_head = sg.units / group, first = KeyTiles::first_tile(a.mask, sg.tile);
+      const int row0 = first_row(a.mask, j);   // the first query row that sees this key
+      int i = first + sg.kb % per_head;
+      for (int u = sg.kb; u < sg.ke; ++u, ++n) {
+        ok = mbar_wait_warp(bar(kKTFull + n % 2), (n / 2) & 1, g) && mbar_wait_warp(bar(kKSFull), n & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        const float4* st = reinterpret_cast<const float4*>(attn_smem + 7 * TO::kBytes + n % 2 * 1024) + 16 * wg;
+        const int hidden = row0 - (i * kRows + 64 * wg);   // this thread's columns below it see nothing
+        float p[64];
+        {
+          uint32_t s[2][32];
+          tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            const float4 l = st[k / 4];
+            const uint32_t* x = &s[k >> 5][k & 31];
+            p[k] = ex2_approx(fmaf(__uint_as_float(x[0]), to_log2, -l.x));
+            p[k + 1] = ex2_approx(fmaf(__uint_as_float(x[1]), to_log2, -l.y));
+            p[k + 2] = ex2_approx(fmaf(__uint_as_float(x[2]), to_log2, -l.z));
+            p[k + 3] = ex2_approx(fmaf(__uint_as_float(x[3]), to_log2, -l.w));
+          }
+        }
+        if (__any_sync(0xffffffffu, hidden > 0)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k < hidden) p[k] = 0.f;
+        }
+        {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) w[k / 2] = pack2<kHalf>(p[k], p[k + 1]);
+          tmem_st32(s_col, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar(kKPReady));
+        ok = mbar_wait_warp(bar(kKDFull), n & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          uint32_t d[2][32], w[32];
+          tmem_ld32x2_wait(dp_col, d[0], dp_col + 32, d[1]);
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            const float4 e = st[32 + k / 4];
+            const uint32_t* x = &d[k >> 5][k & 31];
+            w[k / 2] = pack2<kHalf>(p[k] * (__uint_as_float(x[0]) - e.x), p[k + 1] * (__uint_as_float(x[1]) - e.y));
+            w[k / 2 + 1] =
+                pack2<kHalf>(p[k + 2] * (__uint_as_float(x[2]) - e.z), p[k + 3] * (__uint_as_float(x[3]) - e.w));
+          }
+          tmem_st32(dp_col, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar(kKDReady));
+        warp_arrive(bar(kKTEmpty + n % 2));
+        if (++i == first + per_head) i = first;
+      }
+      if (ok) ok = mbar_wait_warp(bar(kKAccFull), ns & 1, g);
+      if (!ok) break;
+      ++ns;
+      tc_fence_after();
+      ok = write_rows<D, kHalf>(a, sp, sg, (wg ? c_dk : c_dv) + lanes, r, inside, j >= sg.kl, dst,
+                                wg ? a.scale : 1.f, attn_record_floats(D), static_cast<size_t>(wg) * D * kRows,
+                                a.counters + ((static_cast<size_t>(sg.b) * a.Hkv + sg.h) * walk.ntiles + sg.tile) * 2 + wg,
+                                bar(kKGroup + wg), group_phase, bar(kKAccEmpty), &shared->last[wg], g);
+    }
+    __syncwarp();
+    tc_fence_before();
+    warp_arrive(bar(kKFinal));
+  }
+  __syncwarp();
+  if (warp == 1) {
+    // Every MMA is done and every other warp finished with TMEM.
+    mbar_wait_drain(bar(kKFinal), 0);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dq
+enum : int {
+  kQQFull = 0,            // q and do of a segment
+  kQQEmpty,
+  kQKFull,                // + stage (3)
+  kQKEmpty = kQKFull + 3,
+  kQVFull = kQKEmpty + 3,   // + stage (2)
+  kQVEmpty = kQVFull + 2,
+  kQSFull = kQVEmpty + 2,   // + buffer (2)
+  kQDFull = kQSFull + 2,
+  kQDReady,               // 8 warps
+  kQAccFull,
+  kQAccEmpty,             // 8 warps
+  kQGroup,                // + group (2), 4 warps
+  kQSide = kQGroup + 2,
+  kQFinal,                // the MMA warp's commit and 8 warps
+  kQBars
+};
+static_assert(kQBars * 8 <= 320, "control block");
+using QTiles = RowTiles<kRows>;
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    arl2_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                        const __grid_constant__ AttnArgs a) {
+  using TO = TileOf<D>;
+  extern __shared__ __align__(1024) uint8_t attn_smem[];
+  const uint32_t base = smem_u32(attn_smem);
+  const uint32_t q_tile = base, g_tile = base + TO::kBytes, k_ring = base + 2 * TO::kBytes,
+                 v_ring = base + 5 * TO::kBytes, ctl = base + 7 * TO::kBytes;
+  uint8_t* gctl = attn_smem + 7 * TO::kBytes;
+  auto bar = [&](int i) { return ctl + 8u * i; };
+  Ctl* shared = reinterpret_cast<Ctl*>(gctl + 320);
+  const int warp = threadIdx.x >> 5;
+  const Guard g{&shared->abort, a.err, a.timeout_ns};
+  const int group = a.H / a.Hkv;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kQBars; ++i)
+      mbar_init(bar(i), i == kQDReady || i == kQAccEmpty                ? 8
+                        : i == kQGroup || i == kQGroup + 1 ? 4
+                        : i == kQFinal                                 ? 9
+                                                                       : 1);
+    shared->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    if (elect_one()) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      prefetch_tmap(&tm_g);
+    }
+    __syncwarp();
+    make_split<QTiles>(a.mask, a.B, a.H, 1, 4, &shared->split);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = shared->tmem;
+  const uint32_t c_dp = tmem + 256, c_dq = tmem + 384;   // S buffers at 0 and 128
+
+  if (warp == 0) {
+    const Split sp = shared->split;
+    Walk<QTiles> walk(a.mask, sp, a.H, 1);
+    Seg sg;
+    const bool lead = elect_one();
+    uint32_t ns = 0, nk = 0, nv = 0, side_phase = 0;   // copies made
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      if (sg.units == 0) continue;
+      if (ns > 0 && !mbar_wait_warp(bar(kQQEmpty), (ns - 1) & 1, g)) break;
+      if (lead) {
+        mbar_expect_tx(bar(kQQFull), 2 * TO::kBytes);
+        load_tile<D>(q_tile, &tm_q, bar(kQQFull), sg.h, sg.tile * kRows, sg.b);
+        load_tile<D>(g_tile, &tm_g, bar(kQQFull), sg.h, sg.tile * kRows, sg.b);
+      }
+      ++ns;
+      for (int t = sg.kb; t < sg.ke; ++t) {
+        ok = nk < 3 || mbar_wait_warp(bar(kQKEmpty + nk % 3), (nk / 3 - 1) & 1, g);
+        if (!ok) break;
+        const int r0 = sg.kl < a.mask.Tk ? sg.kl - t * kRows : kRows;   // keys behind the length read as zero
+        ok = load_clean<D>(k_ring + nk % 3 * TO::kBytes, &tm_k, bar(kQKFull + nk % 3), bar(kQSide), side_phase,
+                           sg.h / group, t * kRows, sg.b, r0, lead, g);
+        ++nk;
+        if (!ok) break;
+        ok = nv < 2 || mbar_wait_warp(bar(kQVEmpty + nv % 2), (nv / 2 - 1) & 1, g);
+        if (!ok) break;
+        if (lead) {
+          mbar_expect_tx(bar(kQVFull + nv % 2), TO::kBytes);
+          load_tile<D>(v_ring + nv % 2 * TO::kBytes, &tm_v, bar(kQVFull + nv % 2), sg.h / group, t * kRows, sg.b);
+        }
+        ++nv;
+      }
+    }
+    __syncwarp();
+    // Every copy issued lands before the CTA may exit.
+    if (ns > 0) mbar_wait_drain(bar(kQQFull), (ns - 1) & 1);
+    for (uint32_t s = 0; s < 3; ++s)
+      if (nk > s) mbar_wait_drain(bar(kQKFull + s), ((nk - s + 2) / 3 - 1) & 1);
+    for (uint32_t s = 0; s < 2; ++s)
+      if (nv > s) mbar_wait_drain(bar(kQVFull + s), ((nv - s + 1) / 2 - 1) & 1);
+  } else if (warp == 1) {
+    const Split sp = shared->split;
+    Walk<QTiles> walk(a.mask, sp, a.H, 1);
+    Seg sg;
+    const bool lead = elect_one();
+    constexpr uint32_t id_s = attn_idesc<kHalf>(128, false, false), id_d = attn_idesc<kHalf>(D, false, true);
+    uint32_t ns = 0, n = 0;   // segments and units begun
+    bool ok = true;
+    auto k_full = [&](uint32_t i) { return mbar_wait_warp(bar(kQKFull + i % 3), (i / 3) & 1, g); };
+    auto v_full = [&](uint32_t i) { return mbar_wait_warp(bar(kQVFull + i % 2), (i / 2) & 1, g); };
+    auto k_at = [&](uint32_t i) { return k_ring + i % 3 * TO::kBytes; };
+    auto scores = [&](uint32_t i) {   // unit i's S
+      if (!k_full(i)) return false;
+      tc_fence_after();
+      if (lead) {
+        mma_over_d<D>(tmem + 128u * (i & 1), q_tile, k_at(i), id_s);
+        mma_commit(bar(kQSFull + (i & 1)));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto grads = [&](uint32_t i) {   // unit i's dP
+      if (!v_full(i)) return false;
+      tc_fence_after();
+      if (lead) {
+        mma_over_d<D>(c_dp, g_tile, v_ring + i % 2 * TO::kBytes, id_s);
+        mma_commit(bar(kQDFull));
+        mma_commit(bar(kQVEmpty + i % 2));
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next(sg)) {
+      if (sg.units == 0) continue;
+      const int cnt = sg.ke - sg.kb;
+      ok = mbar_wait_warp(bar(kQQFull), ns & 1, g) && scores(n) && grads(n) && (cnt < 2 || scores(n + 1));
+      if (!ok) break;
+      for (int u = 0; u < cnt; ++u, ++n) {
+        ok = mbar_wait_warp(bar(kQDReady), n & 1, g);
+        if (ok && u + 1 < cnt) ok = grads(n + 1);   // first: the next softmax waits for it
+        if (ok && u == 0 && ns > 0) ok = mbar_wait_warp(bar(kQAccEmpty), (ns - 1) & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {
+          mma_over_rows<32>(c_dq, tmem + 128u * (n & 1), k_at(n), id_d, u > 0);
+          mma_commit(bar(kQKEmpty + n % 3));
+        }
+        __syncwarp();
+        if (u + 2 < cnt) ok = scores(n + 2);
+        if (!ok) break;
+      }
+      if (!ok) break;
+      if (lead) {
+        mma_commit(bar(kQAccFull));
+        mma_commit(bar(kQQEmpty));
+      }
+      __syncwarp();
+      ++ns;
+    }
+    __syncwarp();
+    if (lead) mma_commit(bar(kQFinal));
+    __syncwarp();
+  } else if (warp >= 4) {
+    const Split sp = shared->split;
+    Walk<QTiles> walk(a.mask, sp, a.H, 1);
+    Seg sg;
+    constexpr int kCols = D > 32 ? D / 2 : 32;                 // output columns of a group; d = 32: of the first
+    const int wg = (warp >> 2) - 1;                            // score columns 64 wg ..
+    const int r = (warp & 3) * 32 + (threadIdx.x & 31);        // query row == TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
+    const float to_log2 = a.scale * 1.4426950408889634f;
+    const int Tpad = (a.mask.Tq + kRows - 1) / kRows * kRows;
+    const bool writes = D > 32 || wg == 0;
+    uint32_t n = 0, ns = 0, group_phase = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int row = sg.tile * kRows + r;
+      uint16_t* dst = a.o.ptr + sg.b * a.o.sb + row * a.o.st + sg.h * a.o.sh + kCols * wg;
+      const bool inside = row < a.mask.Tq;
+      if (sg.units == 0) {
+        float z[32] = {};
+        for (int k = 0; k < kCols; k += 32)
+          if (inside && writes) store32<kHalf>(dst + k, z);
+        continue;
+      }
+      const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + sg.h) * 2 * Tpad + row;
+      const float lse = st[0], delta = st[Tpad];
+      const int limit = row < sg.ql ? key_limit(a.mask, row, sg.kl) : 0;
+      for (int t = sg.kb; t < sg.ke; ++t, ++n) {
+        ok = mbar_wait_warp(bar(kQSFull + (n & 1)), (n / 2) & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s_col = tmem + lanes + 128u * (n & 1) + 64u * wg, dp_col = c_dp + lanes + 64u * wg;
+        const int seen = limit - (t * kRows + 64 * wg);   // this thread's columns that the row sees
+        float p[64];
+        {
+          uint32_t s[2][32];
+          tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
+#pragma unroll
+          for (int k = 0; k < 64; ++k) p[k] = ex2_approx(fmaf(__uint_as_float(s[k >> 5][k & 31]), to_log2, -lse));
+        }
+        ok = mbar_wait_warp(bar(kQDFull), n & 1, g);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t d[2][32], w[32];
+        tmem_ld32x2_wait(dp_col, d[0], dp_col + 32, d[1]);
+#pragma unroll
+        for (int k = 0; k < 64; ++k) p[k] *= __uint_as_float(d[k >> 5][k & 31]) - delta;
+        if (__any_sync(0xffffffffu, seen < 64)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k >= seen) p[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) w[k / 2] = pack2<kHalf>(p[k], p[k + 1]);
+        tmem_st32(s_col, w);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar(kQDReady));
+      }
+      if (ok) ok = mbar_wait_warp(bar(kQAccFull), ns & 1, g);
+      if (!ok) break;
+      ++ns;
+      tc_fence_after();
+      if (writes)
+        ok = write_rows<kCols, kHalf>(a, sp, sg, c_dq + lanes + kCols * wg, r, inside, row >= sg.ql, dst, a.scale,
+                                      attn_record_floats(D), static_cast<size_t>(wg) * kCols * kRows,
+                                      a.counters + ((static_cast<size_t>(sg.b) * a.H + sg.h) * walk.ntiles + sg.tile) * 2 + wg,
+                                      bar(kQGroup + wg), group_phase, bar(kQAccEmpty), &shared->last[wg], g);
+      else
+        warp_arrive(bar(kQAccEmpty));
+    }
+    __syncwarp();
+    tc_fence_before();
+    warp_arrive(bar(kQFinal));
+  }
+  __syncwarp();
+  if (warp == 1) {
+    // Every MMA is done and every other warp finished with TMEM.
+    mbar_wait_drain(bar(kQFinal), 0);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool kHalf>
+cudaError_t setup() {
+  cudaError_t e = cudaFuncSetAttribute(arl2_attn_dkv_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bwd_smem<D>()));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(arl2_attn_dq_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bwd_smem<D>()));
+}
+template <int D, bool kHalf>
+cudaError_t launch(bool dq, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& g,
+                   const AttnArgs& a, int ctas, cudaStream_t st) {
+  if (dq)
+    arl2_attn_dq_kernel<D, kHalf><<<ctas, kBwdThreads, bwd_smem<D>(), st>>>(q, k, v, g, a);
+  else
+    arl2_attn_dkv_kernel<D, kHalf><<<ctas, kBwdThreads, bwd_smem<D>(), st>>>(q, k, v, g, a);
+  return cudaGetLastError();
+}
+cudaError_t by_type(bool dq, int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                    const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st) {
+  if (half)
+    return d == 32   ? launch<32, true>(dq, q, k, v, g, a, ctas, st)
+           : d == 64 ? launch<64, true>(dq, q, k, v, g, a, ctas, st)
+                     : launch<128, true>(dq, q, k, v, g, a, ctas, st);
+  return d == 32   ? launch<32, false>(dq, q, k, v, g, a, ctas, st)
+         : d == 64 ? launch<64, false>(dq, q, k, v, g, a, ctas, st)
+                   : launch<128, false>(dq, q, k, v, g, a, ctas, st);
+}
+
+}  // namespace
+
+cudaError_t attn_bwd_setup() {
+  cudaError_t e = setup<32, false>();
+  if (e == cudaSuccess) e = setup<64, false>();
+  if (e == cudaSuccess) e = setup<128, false>();
+  if (e == cudaSuccess) e = setup<32, true>();
+  if (e == cudaSuccess) e = setup<64, true>();
+  if (e == cudaSuccess) e = setup<128, true>();
+  return e;
+}
+
+cudaError_t launch_attn_prep(bool half, const AttnPrepArgs& a, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.B) * ((a.Tq + kRows - 1) / kRows * kRows) * a.H;
+  const long long blocks = (rows * (a.d / 8) + 255) / 256;
+  if (half)
+    arl2_attn_prep_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
+  else
+    arl2_attn_prep_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_dkv(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st) {
+  return by_type(false, d, half, q, k, v, g, a, ctas, st);
+}
+cudaError_t launch_attn_dq(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                           const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st) {
+  return by_type(true, d, half, q, k, v, g, a, ctas, st);
+}
+
+}  // namespace arl2

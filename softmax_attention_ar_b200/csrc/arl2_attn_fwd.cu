@@ -1,0 +1,450 @@
+// Softmax attention that keeps its row statistics, for training (arl2_attn_forward):
+//     o = softmax(scale q k^T + mask) v,    lse_i = log sum_j exp(scale q_i.k_j)
+// over the visible keys (arl2_attn.cuh). The 4 d flops per visible pair on the tensor cores
+// bound it; the exponentials come next (16 a clock and SM on the MUFU unit: 1024 clocks for a
+// 128 x 128 tile whose two products take 1024 clocks on the tensor pipe at d = 128).
+//
+// A tile is two 128-row query tiles of one head (256 rows), which share every K and V tile
+// that is loaded. While the softmax of one works on its scores, the tensor pipe does the
+// products of the other. Online softmax: scores in log2 units, the running maximum m raised
+// only when a key tile exceeds it by more than 8, so that the output accumulator is rescaled
+// rarely; m, the sum l and the accumulator are fp32, only the probabilities (below 2^8) are
+// rounded to 16 bits for the second product.
+//
+// Roles (384 threads, one CTA per SM): warp 0 copies (Q per segment; K and V tiles through a
+// ring of 5), warp 1 issues every MMA, warps 4-7 and 8-11 are the softmax of query tile 0 and 1,
+// thread = row = TMEM lane. TMEM: S0, S1 (columns 0, 128; the packed P overwrites the first 64
+// of its S), O0, O1 (256, 384). One issuing thread keeps the MMAs that touch the same columns
+// in order; the rest is ordered by barriers:
+//   - S full (commit) -> softmax; P ready (4 warps) -> P V MMA; the commit of S(t + 1) also says
+//     that P V (t) is done, so the softmax may rescale O before it hands over P (t + 1);
+//   - O full -> epilogue, O empty -> the next segment's first P V.
+#include <algorithm>
+
+#include "arl2_attn_kernels.h"
+
+namespace arl2 {
+namespace {
+
+constexpr int kFwdRows = 256;
+constexpr int kFwdThreads = 384;
+constexpr int kRing = 5;
+using FwdTiles = RowTiles<kFwdRows>;
+enum : int {
+  kFQFull = 0,
+  kFQEmpty = 1,
+  kFFull = 2,              // + stage
+  kFEmpty = kFFull + kRing,
+  kFSFull = kFEmpty + kRing,   // + query tile (2)
+  kFPReady = kFSFull + 2,
+  kFOFull = kFPReady + 2,
+  kFOEmpty = kFOFull + 2,
+  kFGroup = kFOEmpty + 2,
+  kFSide = kFGroup + 2,
+  kFFinal = kFSide + 1,
+  kFBars = kFFinal + 1
+};
+constexpr uint32_t kFCtl = 512;   // barriers, split, flags
+static_assert(kFBars * 8 <= 256 && sizeof(Split) + 32 <= 256, "control block");
+template <int D>
+constexpr uint32_t fwd_smem() {
+  return (2 + kRing) * TileOf<D>::kBytes + kFCtl;
+}
+static_assert(fwd_smem<128>() <= 232448, "shared memory per CTA");
+constexpr float kRaise = 8.0f;    // log2 units
+
+// Per record: [2 query tiles][d / 4 quads][128 rows] float4 of O, then [2][2][128] m and l.
+template <int D>
+__device__ __forceinline__ float* fwd_record(const AttnArgs& a, int slot) {
+  return a.records + static_cast<size_t>(slot) * attn_record_floats(D);
+}
+
+template <int D, bool kHalf>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int b, int h, int row, const float (&x)[32], int c0) {
+  uint16_t* dst = a.o.ptr + b * a.o.sb + row * a.o.st + h * a.o.sh + c0;
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    uint4 v = make_uint4(pack2<kHalf>(x[c], x[c + 1]), pack2<kHalf>(x[c + 2], x[c + 3]),
+                         pack2<kHalf>(x[c + 4], x[c + 5]), pack2<kHalf>(x[c + 6], x[c + 7]));
+    *reinterpret_cast<uint4*>(dst + c) = v;
+  }
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    arl2_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs a) {
+  using TO = TileOf<D>;
+  extern __shared__ __align__(1024) uint8_t attn_smem[];
+  const uint32_t base = smem_u32(attn_smem);
+  const uint32_t ctl = base + (2 + kRing) * TO::kBytes;
+  uint8_t* gctl = attn_smem + (2 + kRing) * TO::kBytes;
+  auto bar = [&](int i) { return ctl + 8u * i; };
+  Split* split = reinterpret_cast<Split*>(gctl + 256);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gctl + 256 + sizeof(Split));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
+  const int warp = threadIdx.x >> 5;
+  const Guard g{abort_flag, a.err, a.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFBars; ++i) {
+      const bool by4 = (i >= kFPReady && i < kFPReady + 2) || (i >= kFOEmpty && i < kFGroup + 2);
+      mbar_init(bar(i), i == kFFinal ? 9 : by4 ? 4 : 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    if (elect_one()) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
+    __syncwarp();
+    make_split<FwdTiles>(a.mask, a.B, a.H, 1, 4, split);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Registers move from the copy and MMA warps to the softmax, which holds a row of 128 scores:
+  // 128 threads x 72 + 256 x 208 = 62464 of the block's 384 x 168.
+  const int group = a.H / a.Hkv;
+  const uint32_t q_tile = base, ring0 = base + 2 * TO::kBytes;
+
+  if (warp == 0) {
+    regs_dec<72>();
+    const Split sp = *split;
+    Walk<FwdTiles> walk(a.mask, sp, a.H, 1);
+    Seg sg;
+    const bool lead = elect_one();
+    uint32_t ns = 0, r = 0, side_phase = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      if (sg.units == 0) continue;
+      if (ns > 0 && !mbar_wait_warp(bar(kFQEmpty), (ns - 1) & 1, g)) break;
+      const int tiles = sg.tile * kFwdRows + kRows < sg.ql ? 2 : 1;
+      if (lead) {
+        mbar_expect_tx(bar(kFQFull), tiles * TO::kBytes);
+        for (int i = 0; i < tiles; ++i)
+          load_tile<D>(q_tile + i * TO::kBytes, &tm_q, bar(kFQFull), sg.h, sg.tile * kFwdRows + i * kRows, sg.b);
+      }
+      ++ns;
+      for (int t = sg.kb; ok && t < sg.ke; ++t) {
+        for (int kv = 0; kv < 2; ++kv, ++r) {
+          const uint32_t st = r % kRing;
+          if (r >= kRing && !mbar_wait_warp(bar(kFEmpty + st), (r / kRing - 1) & 1, g)) {
+            ok = false;
+            break;
+          }
+          // Values behind the length must not reach P V; keys there are masked in the scores.
+          const int r0 = kv == 1 && sg.kl < a.mask.Tk ? sg.kl - t * kRows : kRows;
+          if (!load_clean<D>(ring0 + st * TO::kBytes, kv ? &tm_v : &tm_k, bar(kFFull + st), bar(kFSide), side_phase,
+                             sg.h / group, t * kRows, sg.b, r0, lead, g)) {
+            ++r;
+            ok = false;
+            break;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    // Every copy issued lands before the CTA may exit.
+    if (ns > 0) mbar_wait_drain(bar(kFQFull), (ns - 1) & 1);
+    for (uint32_t st = 0; st < kRing; ++st) {
+      const uint32_t uses = r > st ? (r - st + kRing - 1) / kRing : 0;
+      if (uses) mbar_wait_drain(bar(kFFull + st), (uses - 1) & 1);
+    }
+  } else if (warp == 1) {
+    regs_dec<72>();
+    const Split sp = *split;
+    Walk<FwdTiles> walk(a.mask, sp, a.H, 1);
+    Seg sg;
+    const bool lead = elect_one();
+    constexpr uint32_t id_s = attn_idesc<kHalf>(128, false, false), id_o = attn_idesc<kHalf>(D, false, true);
+    uint32_t ns = 0, r = 0, np[2] = {0, 0}, nseg[2] = {0, 0};
+    bool ok = true;
+    auto full = [&](uint32_t i) { return mbar_wait_warp(bar(kFFull + i % kRing), (i / kRing) & 1, g); };
+    auto slot = [&](uint32_t i) { return ring0 + (i % kRing) * TO::kBytes; };
+    while (ok && walk.next(sg)) {
+      if (sg.units == 0) continue;
+      const int tiles = sg.tile * kFwdRows + kRows < sg.ql ? 2 : 1;
+      const int n = sg.ke - sg.kb;
+      ok = mbar_wait_warp(bar(kFQFull), ns & 1, g) && full(r);
+      if (!ok) break;
+      tc_fence_after();
+      if (lead) {
+        for (int i = 0; i < tiles; ++i) {
+          mma_over_d<D>(tmem + 128u * i, q_tile + i * TO::kBytes, slot(r), id_s);
+          mma_commit(bar(kFSFull + i));
+        }
+        mma_commit(bar(kFEmpty + r % kRing));
+      }
+      __syncwarp();
+      for (int t = 0; ok && t < n; ++t, r += 2) {
+        const bool more = t + 1 < n;
+        for (int i = 0; i < tiles; ++i) {
+          ok = mbar_wait_warp(bar(kFPReady + i), np[i] & 1, g);
+          if (ok && t == 0 && nseg[i] > 0) ok = mbar_wait_warp(bar(kFOEmpty + i), (nseg[i] - 1) & 1, g);
+          if (ok && i == 0) ok = full(r + 1);
+          if (!ok) break;
+          ++np[i];
+          tc_fence_after();
+          if (lead) {
+            mma_over_rows<0>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, t > 0);
+            if (i + 1 == tiles) mma_commit(bar(kFEmpty + (r + 1) % kRing));
+          }
+          __syncwarp();
+          if (more) {
+            if (i == 0) ok = full(r + 2);
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+              mma_over_d<D>(tmem + 128u * i, q_tile + i * TO::kBytes, slot(r + 2), id_s);
+              mma_commit(bar(kFSFull + i));
+              if (i + 1 == tiles) mma_commit(bar(kFEmpty + (r + 2) % kRing));
+            }
+          } else if (lead) {
+            mma_commit(bar(kFOFull + i));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (lead) mma_commit(bar(kFQEmpty));
+      __syncwarp();
+      ++ns;
+      for (int i = 0; i < tiles; ++i) ++nseg[i];
+    }
+    __syncwarp();
+    if (lead) mma_commit(bar(kFFinal));
+    __syncwarp();
+  } else if (warp < 4) {
+    regs_dec<72>();
+  } else {
+    regs_inc<208>();
+    const Split sp = *split;
+    Walk<FwdTiles> walk(a.mask, sp, a.H, 1);
+    Seg sg;
+    const int i = (warp >> 2) - 1;                              // query tile
+    const int r = (warp & 3) * 32 + (threadIdx.x & 31);         // its row == TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
+    const uint32_t s_col = tmem + lanes + 128u * i, o_col = tmem + lanes + 256u + 128u * i;
+    const float to_log2 = a.scale * 1.4426950408889634f;
+    uint32_t nt = 0, nseg = 0, group_phase = 0;
+    const int c = static_cast<int>(blockIdx.x);
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int row = sg.tile * kFwdRows + i * kRows + r;
+      const bool in_q = row < sg.ql;
+      float* lse = a.lse + (static_cast<size_t>(sg.b) * a.H + sg.h) * a.mask.Tq;
+      if (sg.units == 0 || sg.tile * kFwdRows + i * kRows >= sg.ql) {
+        // Nothing to see, or rows behind the length: zeros, once per tile.
+        if (sg.kb == 0 && row < a.mask.Tq) {
+          float z[32] = {};
+#pragma unroll
+          for (int k = 0; k < D; k += 32) store_row<D, kHalf>(a, sg.b, sg.h, row, z, k);
+          lse[row] = -INFINITY;
+        }
+        continue;
+      }
+      const int limit = in_q ? key_limit(a.mask, row, sg.kl) : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int t = sg.kb; t < sg.ke; ++t) {
+        ok = mbar_wait_warp(bar(kFSFull + i), nt & 1, g);
+        if (!ok) break;
+        ++nt;
+        tc_fence_after();
+        uint32_t s[4][32];
+        tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
+        tmem_ld32x2_wait(s_col + 64, s[2], s_col + 96, s[3]);
+        const int seen = limit - t * kRows;   // columns of this tile that the row sees
+        if (__any_sync(0xffffffffu, seen < kRows)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * q + k >= seen) s[q][k] = 0xff800000u;   // -inf
+        }
+        float top[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          top[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+          for (int k = 2; k < 32; k += 2) top[q] = fmax3(top[q], __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
+        }
+        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * to_log2;
+        const bool raise = tile_top > m + kRaise || (m == -INFINITY && tile_top > m);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float m_new = raise ? tile_top : m;
+          const float f = raise && m != -INFINITY ? ex2_approx(m - m_new) : 1.f;
+          l *= f;
+          m = m_new;
+          if (t > sg.kb) {
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+              uint32_t x[32];
+              tmem_ld32_wait(o_col + k, x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+              tmem_st32(o_col + k, x);
+            }
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(s[q][k]), to_log2, -shift));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(s[q][k + 1]), to_log2, -shift));
+            sum[(k >> 1) & 3] += p0 + p1;
+            p[k >> 1] = pack2<kHalf>(p0, p1);
+          }
+          tmem_st16(s_col + 16 * q, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar(kFPReady + i));
+      }
+      if (ok) ok = mbar_wait_warp(bar(kFOFull + i), nseg & 1, g);
+      if (!ok) break;
+      ++nseg;
+      tc_fence_after();
+      if (sg.whole) {
+        const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          uint32_t x[32];
+          float y[32];
+          tmem_ld32_wait(o_col + k, x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = in_q && limit > 0 ? __uint_as_float(x[e]) * f : 0.f;
+          if (row < a.mask.Tq) store_row<D, kHalf>(a, sg.b, sg.h, row, y, k);
+        }
+        tc_fence_before();
+        warp_arrive(bar(kFOEmpty + i));
+        if (row < a.mask.Tq) lse[row] = in_q && limit > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        continue;
+      }
+      // A part of the tile: its record, then the last to arrive adds them up.
+      float* rec = fwd_record<D>(a, record_slot(sp, c, sg.first));
+      float4* ro = reinterpret_cast<float4*>(rec) + i * (D / 4) * kRows;
+      float* rml = rec + 2 * kRows * D + i * 2 * kRows;
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t x[32];
+        tmem_ld32_wait(o_col + k, x);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          ro[(k + e) / 4 * kRows + r] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                   __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+      }
+      tc_fence_before();
+      warp_arrive(bar(kFOEmpty + i));
+      rml[r] = m;
+      rml[kRows + r] = l;
+      __threadfence();
+      ok = warps_sync(bar(kFGroup + i), group_phase, g);
+      if (!ok) break;
+      const int c0 = unit_owner(sp, sg.first), c1 = unit_owner(sp, sg.first + sg.units - 1);
+      unsigned int* counter =
+          a.counters + ((static_cast<size_t>(sg.b) * a.H + sg.h) * walk.ntiles + sg.tile) * 2 + i;
+      if (r == 0) {
+        const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c1 - c0);
+        if (last) *counter = 0;
+        last_flag[i] = last;
+      }
+      ok = warps_sync(bar(kFGroup + i), group_phase, g);
+      if (!ok) break;
+      if (!last_flag[i]) continue;
+      __threadfence();
+      float m_all = -INFINITY, l_all = 0.f;
+      for (int j = c0; j <= c1; ++j) {
+        const float* ml = fwd_record<D>(a, record_slot(sp, j, sg.first)) + 2 * kRows * D + i * 2 * kRows;
+        const float mj = __ldcg(ml + r), lj = __ldcg(ml + kRows + r);
+        if (mj > m_all) {
+          l_all = m_all == -INFINITY ? lj : fmaf(l_all, exp2f(m_all - mj), lj);
+          m_all = mj;
+        } else {
+          l_all += mj == -INFINITY ? lj : lj * exp2f(mj - m_all);
+        }
+      }
+      const float f = l_all > 0.f || l_all != l_all ? 1.f / l_all : 0.f;
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        float y[32] = {};
+        for (int j = c0; j <= c1; ++j) {
+          const float* rj = fwd_record<D>(a, record_slot(sp, j, sg.first));
+          const float4* oj = reinterpret_cast<const float4*>(rj) + i * (D / 4) * kRows;
+          const float mj = __ldcg(rj + 2 * kRows * D + i * 2 * kRows + r);
+          const float w = mj == -INFINITY ? 0.f : exp2f(mj - m_all) * f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 v = __ldcg(oj + (k + e) / 4 * kRows + r);
+            y[e] = fmaf(v.x, w, y[e]);
+            y[e + 1] = fmaf(v.y, w, y[e + 1]);
+            y[e + 2] = fmaf(v.z, w, y[e + 2]);
+            y[e + 3] = fmaf(v.w, w, y[e + 3]);
+          }
+        }
+        if (!(in_q && limit > 0)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.f;
+        }
+        if (row < a.mask.Tq) store_row<D, kHalf>(a, sg.b, sg.h, row, y, k);
+      }
+      if (row < a.mask.Tq) lse[row] = in_q && limit > 0 ? (m_all + log2f(l_all)) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncwarp();
+    tc_fence_before();
+    warp_arrive(bar(kFFinal));
+  }
+  __syncwarp();
+  if (warp == 1) {
+    // Every MMA is done and every softmax warp finished with TMEM.
+    mbar_wait_drain(bar(kFFinal), 0);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool kHalf>
+cudaError_t setup() {
+  return cudaFuncSetAttribute(arl2_attn_fwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(fwd_smem<D>()));
+}
+template <int D, bool kHalf>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas,
+                   cudaStream_t st) {
+  arl2_attn_fwd_kernel<D, kHalf><<<ctas, kFwdThreads, fwd_smem<D>(), st>>>(q, k, v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_fwd_setup() {
+  cudaError_t e = setup<32, false>();
+  if (e == cudaSuccess) e = setup<64, false>();
+  if (e == cudaSuccess) e = setup<128, false>();
+  if (e == cudaSuccess) e = setup<32, true>();
+  if (e == cudaSuccess) e = setup<64, true>();
+  if (e == cudaSuccess) e = setup<128, true>();
+  return e;
+}
+
+cudaError_t launch_attn_fwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const AttnArgs& a, int ctas, cudaStream_t st) {
+  if (half)
+    return d == 32 ? launch<32, true>(q, k, v, a, ctas, st)
+                   : d == 64 ? launch<64, true>(q, k, v, a, ctas, st) : launch<128, true>(q, k, v, a, ctas, st);
+  return d == 32 ? launch<32, false>(q, k, v, a, ctas, st)
+                 : d == 64 ? launch<64, false>(q, k, v, a, ctas, st) : launch<128, false>(q, k, v, a, ctas, st);
+}
+
+}  // namespace arl2

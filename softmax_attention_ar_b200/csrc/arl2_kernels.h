@@ -176,6 +176,10 @@ cudaError_t launch_gates(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const
 int prepare_device(int* dev, int* sms);
 bool encode_act_map(CUtensorMap* m, const void* ptr, int B, int L, int H, int d);
 bool encode_mat_map(CUtensorMap* m, const void* ptr, int n, int d);
+// 128-row boxes of a [B, T, heads, d] tensor of 16-bit elements, strides in elements (the map's
+// type says bf16; a copy moves the bits, so fp16 reads through it just as well).
+bool encode_strided_map(CUtensorMap* m, const void* ptr, int B, int T, int heads, int d, long long sb, long long st,
+                        long long sh);
 
 size_t query_smem_bytes();
 size_t commit_smem_bytes();
