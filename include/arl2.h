@@ -340,7 +340,7 @@ typedef struct {
 
 /* Create a context for B sequences of H query and H_kv key heads, up to max_Tq queries and
  * max_Tk keys (at most 2^28), on the current device. It allocates the scratch of both calls
- * (about 40 MB at d = 128, plus 8 bytes per query row and head) and no call allocates more.
+ * (about 60 MB at d = 128, plus 8 bytes per query row and head) and no call allocates more.
  * Calls with smaller Tq and Tk are served by the same context. The device must be current in
  * every call. Calls on one context, replays of captured ones included, share its scratch: they
  * must be ordered, normally by one stream. */

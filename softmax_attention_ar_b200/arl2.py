@@ -79,22 +79,13 @@ _TENSOR = "P3q"
 _ATTN_FWD = struct.Struct(_ATTN_SHAPE + 4 * _TENSOR + "P")
 _ATTN_BWD = struct.Struct(_ATTN_SHAPE + 8 * _TENSOR + "P")
 
+_SCAN_SHAPE = "6iP"
+_SCAN_FWD = struct.Struct(_SCAN_SHAPE + "6P7q")
+_SCAN_BWD = struct.Struct(_SCAN_SHAPE + "9P9q")
+
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # arl2_dtype
 
 
-class _ScanShape(ctypes.Structure):
-    _fields_ = [("B", _I), ("T", _I), ("C", _I), ("heads", _I), ("dtype", _I), ("gate_dtype", _I), ("lens", _P)]
-
-
-class _ScanFwd(ctypes.Structure):
-    _fields_ = [("shape", _ScanShape), ("x", _P), ("a", _P), ("h0", _P), ("h", _P), ("final_state", _P),
-                ("workspace", _P), ("x_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2)]
-
-
-class _ScanBwd(ctypes.Structure):
-    _fields_ = [("shape", _ScanShape), ("dh", _P), ("a", _P), ("h", _P), ("h0", _P), ("dfinal", _P), ("dx", _P),
-                ("da", _P), ("dh0", _P), ("workspace", _P), ("dh_stride", _I64 * 2), ("a_stride", _I64 * 3), ("h_stride", _I64 * 2),
-                ("dx_stride", _I64 * 2)]
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -433,97 +424,99 @@ class KVCacheBaseline:
 
 
 # ------------------------------------------------- training operators: the gated recurrence
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _OnStream:
-    """The device and stream of a call whose tensors may live on a device that is not current.
+    """The stream of a call that was given one, or whose tensors' device is not current.
 
-    With stream=None the call runs on the current stream of the tensors' device, as torch's
-    own operators do. With a stream given, outputs are allocated for that stream and the inputs
-    are recorded on it, so that the allocator does not hand their memory on while the call
-    still reads it.
+    Without a stream the call runs on the current stream of the tensors' device, as torch's own
+    operators do. With one, outputs are allocated for that stream and the inputs are recorded on
+    it, so that the allocator does not hand their memory on while the call still reads it.
     """
-    __slots__ = ("ctx", "ptr")
 
-    def __init__(self, device, stream, inputs):
-        self.ctx = None
+    def __init__(self, index, stream, tensors):
         if stream is None:
-            if device.index != torch.cuda.current_device():
-                self.ctx = torch.cuda.device(device)
-            self.ptr = torch.cuda.current_stream(device).cuda_stream
+            self.ptr = _raw_stream(index)
+            self.ctx = torch.cuda.device(index)
             return
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream.device != device:
-            raise ValueError(f"stream: on {stream.device}, the tensors on {device}")
+            stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+        if stream.device.index != index:
+            raise ValueError(f"stream: on {stream.device}, the tensors on cuda:{index}")
         self.ptr = stream.cuda_stream
         self.ctx = torch.cuda.stream(stream)
-        for t in inputs:
-            if t is not None:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
                 t.record_stream(stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.ctx.__enter__()
         return self.ptr
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _want(t, name, device, dtypes, shape, contiguous=False):
-    """Check one tensor argument (None passes)."""
+def _want(t, name, index, dtypes, shape, contiguous=False):
+    """Check one tensor argument: a CUDA tensor on device `index`; None passes."""
     if t is None:
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected a tensor on cuda:{index}")
     if t.dtype not in dtypes or t.shape != shape:
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    if not contiguous and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+    elif t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: its last dimension must be adjacent in memory")
 
 
-def _cuda_device(t, name):
-    if not isinstance(t, torch.Tensor):
+_F32, _I32 = (torch.float32,), (torch.int32,)
+
+
+def _scan_shape(x, a, lens, name):
+    """Check the values and gates of a call; (device index, shape, strides of the gates, the
+    fields of arl2_scan_shape)."""
+    if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    if not x.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    return t.device
-
-
-def _scan_args(x, a, lens, name):
-    device = _cuda_device(x, name)
-    if x.dim() != 3 or x.dtype not in DTYPES:
-        raise ValueError(f"{name}: expected bf16, fp16 or fp32 [B, T, C], got {x.dtype} {tuple(x.shape)}")
-    B, T, C = x.shape
+    dtype, shape, index = x.dtype, x.shape, x.get_device()
+    if len(shape) != 3 or dtype not in DTYPES:
+        raise ValueError(f"{name}: expected bf16, fp16 or fp32 [B, T, C], got {dtype} {tuple(shape)}")
+    _want(x, name, index, (dtype,), shape)
+    B, T, C = shape
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
         raise TypeError("a must be a torch.Tensor [B, T, C] or [B, heads, T]")
-    # A gate tensor of x's shape is per channel; one whose last dimension is T is per head.
-    heads = 0 if a.shape == x.shape else a.shape[1]
-    if heads:
-        if a.device != device or a.dtype != torch.float32 or a.shape != (B, heads, T) or heads < 1 or C % heads:
-            raise ValueError(f"a: expected gates {(B, T, C)}, or fp32 [B, heads, T] with heads dividing {C}, got "
-                             f"{a.dtype} {tuple(a.shape)}")
-        sa = a.stride()
-        a_stride = (sa[0], sa[2], sa[1])
+    # A gate tensor of x's shape is per channel; otherwise it is per head.
+    st = a.stride()
+    if a.shape == shape:
+        heads = 0
+        _want(a, "a", index, (dtype, torch.float32), shape)
     else:
-        _want(a, "a", device, (x.dtype, torch.float32), x.shape)
-        a_stride = (a.stride(0), a.stride(1), 0)
-    _want(lens, "lens", device, (torch.int32,), (B,), True)
-    return device, _ScanShape(B, T, C, heads, DTYPES[x.dtype], DTYPES[a.dtype], _ptr(lens)), a_stride
+        heads = a.shape[1]
+        if a.get_device() != index or a.dtype != torch.float32 or a.shape != (B, heads, T) or heads < 1 or C % heads:
+            raise ValueError(f"a: expected gates {(B, T, C)}, or fp32 [B, heads, T] with heads dividing {C}, got "
+                             f"{a.dtype} {tuple(a.shape)} on {a.device}")
+        st = (st[0], st[2], st[1])
+    if lens is not None:
+        _want(lens, "lens", index, _I32, (B,), True)
+    return index, shape, st, (B, T, C, heads, DTYPES[dtype], DTYPES[a.dtype], _ptr(lens))
 
 
-def _scan_workspace(shape, device):
-    n = load_library().arl2_scan_workspace_bytes(ctypes.byref(shape))
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+def _scan_workspace(lib, fields, x):
+    n = lib.arl2_scan_workspace_bytes(struct.pack(_SCAN_SHAPE, *fields))
+    return x.new_empty(n, dtype=torch.uint8) if n else None
 
 
 def scan_forward(x, a, h0=None, lens=None, out=None, final=None, stream=None):
@@ -531,25 +524,35 @@ def scan_forward(x, a, h0=None, lens=None, out=None, final=None, stream=None):
 
     x bf16, fp16 or fp32 [B, T, C]; a the gates, [B, T, C] of x's type or fp32, or one per head
     and token, fp32 [B, heads, T] with C / heads in {32, 64, 128} (the layout of
-    ``ARL2Layer.gates``); where both shapes fit, per channel is meant. h0 fp32 [B, C], 0 if
-    None. lens int32 [B]: behind lens[b] h is 0, and the final state is that of the last token
-    inside. With T = 1 this is the serving step. out may be x, final may be h0.
+    ``ARL2Layer.gates``). h0 fp32 [B, C], 0 if None. lens int32 [B]: behind lens[b] h is 0, and
+    the final state is that of the last token inside. With T = 1 this is the serving step. out
+    may be x, final may be h0.
     """
-    device, shape, a_stride = _scan_args(x, a, lens, "x")
-    B, T, C = x.shape
-    _want(x, "x", device, (x.dtype,), x.shape)
-    _want(h0, "h0", device, (torch.float32,), (B, C), True)
-    _want(out, "out", device, (x.dtype,), x.shape)
-    _want(final, "final", device, (torch.float32,), (B, C), True)
-    with _OnStream(device, stream, (x, a, h0, lens, out, final)) as st:
-        if out is None:
-            out = torch.empty((B, T, C), dtype=x.dtype, device=device)
-        if final is None:
-            final = torch.empty((B, C), dtype=torch.float32, device=device)
-        ws = _scan_workspace(shape, device)
-        f = _ScanFwd(shape, x.data_ptr(), a.data_ptr(), _ptr(h0), out.data_ptr(), final.data_ptr(), _ptr(ws),
-                     x.stride()[:2], a_stride, out.stride()[:2])
-        _check(load_library().arl2_scan_forward(ctypes.byref(f), st), "arl2_scan_forward")
+    index, shape, st_a, fields = _scan_shape(x, a, lens, "x")
+    B, T, C = shape
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _OnStream(index, stream, (x, a, h0, lens, out, final)) as ptr:
+            return _scan_forward(x, a, h0, out, final, ptr, index, shape, st_a, fields)
+    return _scan_forward(x, a, h0, out, final, _raw_stream(index), index, shape, st_a, fields)
+
+
+def _scan_forward(x, a, h0, out, final, stream, index, shape, st_a, fields):
+    B, _, C = shape
+    lib = load_library()
+    _want(h0, "h0", index, _F32, (B, C), True)
+    if out is None:
+        out = x.new_empty(shape)
+    else:
+        _want(out, "out", index, (x.dtype,), shape)
+    if final is None:
+        final = x.new_empty((B, C), dtype=torch.float32)
+    else:
+        _want(final, "final", index, _F32, (B, C), True)
+    ws = _scan_workspace(lib, fields, x)
+    sx, so = x.stride(), out.stride()
+    f = _SCAN_FWD.pack(*fields, x.data_ptr(), a.data_ptr(), _ptr(h0), out.data_ptr(), final.data_ptr(), _ptr(ws), sx[0],
+                       sx[1], *st_a, so[0], so[1])
+    _check(lib.arl2_scan_forward(f, stream), "arl2_scan_forward")
     return out, final
 
 
@@ -560,29 +563,39 @@ def scan_backward(dh, a, h, h0=None, dfinal=None, lens=None, dx=None, da=None, d
     output; dfinal fp32 [B, C] the gradient of the final state (0 if None). dx has dh's type;
     da the type and shape of a, contiguous; dh0 fp32 [B, C]. dx may be dh.
     """
-    device, shape, a_stride = _scan_args(dh, a, lens, "dh")
-    B, T, C = dh.shape
-    _want(dh, "dh", device, (dh.dtype,), dh.shape)
+    index, shape, st_a, fields = _scan_shape(dh, a, lens, "dh")
     if h is None:
         raise TypeError("h must be a torch.Tensor")
-    _want(h, "h", device, (dh.dtype,), dh.shape)
-    _want(h0, "h0", device, (torch.float32,), (B, C), True)
-    _want(dfinal, "dfinal", device, (torch.float32,), (B, C), True)
-    _want(dx, "dx", device, (dh.dtype,), dh.shape)
-    _want(da, "da", device, (a.dtype,), a.shape, True)
-    _want(dh0, "dh0", device, (torch.float32,), (B, C), True)
-    with _OnStream(device, stream, (dh, a, h, h0, dfinal, lens, dx, da, dh0)) as st:
-        if dx is None:
-            dx = torch.empty((B, T, C), dtype=dh.dtype, device=device)
-        if da is None:
-            da = torch.empty(a.shape, dtype=a.dtype, device=device)
-        if dh0 is None:
-            dh0 = torch.empty((B, C), dtype=torch.float32, device=device)
-        ws = _scan_workspace(shape, device)
-        f = _ScanBwd(shape, dh.data_ptr(), a.data_ptr(), h.data_ptr(), _ptr(h0), _ptr(dfinal), dx.data_ptr(),
-                     da.data_ptr(), dh0.data_ptr(), _ptr(ws), dh.stride()[:2], a_stride, h.stride()[:2],
-                     dx.stride()[:2])
-        _check(load_library().arl2_scan_backward(ctypes.byref(f), st), "arl2_scan_backward")
+    _want(h, "h", index, (dh.dtype,), shape)
+    args = (dh, a, h, h0, dfinal, dx, da, dh0)
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _OnStream(index, stream, args + (lens,)) as ptr:
+            return _scan_backward(*args, ptr, index, shape, st_a, fields)
+    return _scan_backward(*args, _raw_stream(index), index, shape, st_a, fields)
+
+
+def _scan_backward(dh, a, h, h0, dfinal, dx, da, dh0, stream, index, shape, st_a, fields):
+    B, _, C = shape
+    lib = load_library()
+    _want(h0, "h0", index, _F32, (B, C), True)
+    _want(dfinal, "dfinal", index, _F32, (B, C), True)
+    if dx is None:
+        dx = dh.new_empty(shape)
+    else:
+        _want(dx, "dx", index, (dh.dtype,), shape)
+    if da is None:
+        da = a.new_empty(a.shape)
+    else:
+        _want(da, "da", index, (a.dtype,), a.shape, True)
+    if dh0 is None:
+        dh0 = dh.new_empty((B, C), dtype=torch.float32)
+    else:
+        _want(dh0, "dh0", index, _F32, (B, C), True)
+    ws = _scan_workspace(lib, fields, dh)
+    sg, sh, sx = dh.stride(), h.stride(), dx.stride()
+    f = _SCAN_BWD.pack(*fields, dh.data_ptr(), a.data_ptr(), h.data_ptr(), _ptr(h0), _ptr(dfinal), dx.data_ptr(),
+                       da.data_ptr(), dh0.data_ptr(), _ptr(ws), sg[0], sg[1], *st_a, sh[0], sh[1], sx[0], sx[1])
+    _check(lib.arl2_scan_backward(f, stream), "arl2_scan_backward")
     return dx, da, dh0
 
 
@@ -618,6 +631,7 @@ class SoftmaxAttention:
             raise ValueError(f"device: expected a CUDA device, got {self.device}")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         out = _P()
         with torch.cuda.device(self.device):
             _check(self._lib.arl2_attn_create(B, H, self.H_kv, max_Tq, max_Tk, d, DTYPES[dtype], ctypes.byref(out)),
@@ -646,47 +660,52 @@ class SoftmaxAttention:
             raise Arl2Error(ARL2_ERR_INVALID_ARG, "a closed SoftmaxAttention")
         return q.shape[1], k.shape[1]
 
-    def _check(self, t, name, shape):
+    def _tensor(self, t, name, shape):
+        """Check one [B, T, heads, d] tensor; the fields of its arl2_tensor."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != self.device or t.dtype != self.dtype or t.shape != shape or t.stride(3) != 1:
+        s = t.stride()
+        if t.get_device() != self._index or t.dtype is not self.dtype or t.shape != shape or s[3] != 1:
             raise ValueError(f"{name}: expected {self.dtype} {tuple(shape)} on {self.device}, its last dimension "
-                             f"adjacent in memory; got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-
-    def _check_lse(self, lse, Tq):
-        _want(lse, "lse", self.device, (torch.float32,), (self.B, self.H, Tq), True)
+                             f"adjacent in memory; got {t.dtype} {tuple(t.shape)} on {t.device}, strides {s}")
+        return t.data_ptr(), s[0], s[1], s[2]
 
     def _shape(self, Tq, Tk, q_len, k_len, frame_len, q_start, scale):
-        _want(q_len, "q_len", self.device, (torch.int32,), (self.B,), True)
-        _want(k_len, "k_len", self.device, (torch.int32,), (self.B,), True)
+        """Check the mask and scale; the fields of arl2_attn_shape."""
+        if q_len is not None:
+            _want(q_len, "q_len", self._index, _I32, (self.B,), True)
+        if k_len is not None:
+            _want(k_len, "k_len", self._index, _I32, (self.B,), True)
         for v, name in ((frame_len, "frame_len"), (q_start, "q_start")):
             if not -(1 << 31) <= v < 1 << 31:
                 raise ValueError(f"{name}: {v} does not fit an int")
-        if scale is not None and not 0.0 < scale < float("inf"):
+        if scale is None:
+            scale = 0.0
+        elif not 0.0 < scale < float("inf"):
             raise ValueError(f"scale: expected a positive number, got {scale}")
-        return (Tq, Tk, _ptr(q_len) or 0, _ptr(k_len) or 0, frame_len, q_start, 0.0 if scale is None else scale)
+        return Tq, Tk, _ptr(q_len), _ptr(k_len), frame_len, q_start, scale
 
     def forward(self, q, k, v, out=None, lse=None, q_len=None, k_len=None, frame_len: int = 0, q_start: int = 0,
                 scale: Optional[float] = None, stream=None):
         """o = softmax(scale q k^T + mask) v and the rows' lse; returns (o, lse)."""
         Tq, Tk = self._lengths(q, k)
-        qs, ks = (self.B, Tq, self.H, self.d), (self.B, Tk, self.H_kv, self.d)
-        self._check(q, "q", qs)
-        self._check(k, "k", ks)
-        self._check(v, "v", ks)
         shape = self._shape(Tq, Tk, q_len, k_len, frame_len, q_start, scale)
-        with _OnStream(self.device, stream, (q, k, v, out, lse, q_len, k_len)) as st:
-            if out is None:
-                out = torch.empty(qs, dtype=self.dtype, device=self.device)
-            else:
-                self._check(out, "out", qs)
-            if lse is None:
-                lse = torch.empty((self.B, self.H, Tq), dtype=torch.float32, device=self.device)
-            else:
-                self._check_lse(lse, Tq)
-            f = _ATTN_FWD.pack(*shape, q.data_ptr(), *q.stride()[:3], k.data_ptr(), *k.stride()[:3], v.data_ptr(),
-                               *v.stride()[:3], out.data_ptr(), *out.stride()[:3], lse.data_ptr())
-            _check(self._lib.arl2_attn_forward(self._c, f, st), "arl2_attn_forward")
+        if stream is not None or self._index != torch._C._cuda_getDevice():
+            with _OnStream(self._index, stream, (q, k, v, out, lse, q_len, k_len)) as ptr:
+                return self._forward(q, k, v, out, lse, shape, ptr)
+        return self._forward(q, k, v, out, lse, shape, _raw_stream(self._index))
+
+    def _forward(self, q, k, v, out, lse, shape, stream):
+        qs, ks = (self.B, shape[0], self.H, self.d), (self.B, shape[1], self.H_kv, self.d)
+        fields = self._tensor(q, "q", qs) + self._tensor(k, "k", ks) + self._tensor(v, "v", ks)
+        if out is None:
+            out = q.new_empty(qs)
+        if lse is None:
+            lse = q.new_empty((self.B, self.H, shape[0]), dtype=torch.float32)
+        else:
+            _want(lse, "lse", self._index, _F32, (self.B, self.H, shape[0]), True)
+        f = _ATTN_FWD.pack(*shape, *fields, *self._tensor(out, "out", qs), lse.data_ptr())
+        _check(self._lib.arl2_attn_forward(self._c, f, stream), "arl2_attn_forward")
         return out, lse
 
     def backward(self, do, q, k, v, o, lse, dq=None, dk=None, dv=None, q_len=None, k_len=None, frame_len: int = 0,
@@ -694,28 +713,27 @@ class SoftmaxAttention:
         """The gradients of q, k and v from do, with o and lse of the forward call and its mask
         and scale; returns (dq, dk, dv)."""
         Tq, Tk = self._lengths(q, k)
-        qs, ks = (self.B, Tq, self.H, self.d), (self.B, Tk, self.H_kv, self.d)
-        for t, name, s in ((do, "do", qs), (q, "q", qs), (k, "k", ks), (v, "v", ks), (o, "o", qs)):
-            self._check(t, name, s)
+        shape = self._shape(Tq, Tk, q_len, k_len, frame_len, q_start, scale)
+        args = (do, q, k, v, o, lse, dq, dk, dv)
+        if stream is not None or self._index != torch._C._cuda_getDevice():
+            with _OnStream(self._index, stream, args + (q_len, k_len)) as ptr:
+                return self._backward(*args, shape, ptr)
+        return self._backward(*args, shape, _raw_stream(self._index))
+
+    def _backward(self, do, q, k, v, o, lse, dq, dk, dv, shape, stream):
+        qs, ks = (self.B, shape[0], self.H, self.d), (self.B, shape[1], self.H_kv, self.d)
+        fields = (self._tensor(q, "q", qs) + self._tensor(k, "k", ks) + self._tensor(v, "v", ks)
+                  + self._tensor(o, "o", qs) + self._tensor(do, "do", qs))
         if lse is None:
             raise TypeError("lse must be a torch.Tensor")
-        self._check_lse(lse, Tq)
-        shape = self._shape(Tq, Tk, q_len, k_len, frame_len, q_start, scale)
-        with _OnStream(self.device, stream, (do, q, k, v, o, lse, dq, dk, dv, q_len, k_len)) as st:
-            outs = []
-            for t, name, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks)):
-                if t is None:
-                    t = torch.empty(s, dtype=self.dtype, device=self.device)
-                else:
-                    self._check(t, name, s)
-                outs.append(t)
-            fields = []
-            for t in (q, k, v, o, do, *outs):
-                fields.append(t.data_ptr())
-                fields += t.stride()[:3]
-            f = _ATTN_BWD.pack(*shape, *fields, lse.data_ptr())
-            _check(self._lib.arl2_attn_backward(self._c, f, st), "arl2_attn_backward")
-        return tuple(outs)
+        _want(lse, "lse", self._index, _F32, (self.B, self.H, shape[0]), True)
+        dq = q.new_empty(qs) if dq is None else dq
+        dk = q.new_empty(ks) if dk is None else dk
+        dv = q.new_empty(ks) if dv is None else dv
+        f = _ATTN_BWD.pack(*shape, *fields, *self._tensor(dq, "dq", qs), *self._tensor(dk, "dk", ks),
+                           *self._tensor(dv, "dv", ks), lse.data_ptr())
+        _check(self._lib.arl2_attn_backward(self._c, f, stream), "arl2_attn_backward")
+        return dq, dk, dv
 
     def status(self) -> int:
         """Synchronise and return (and clear) the device status (ARL2_OK, ARL2_ERR_TIMEOUT, ...)."""

@@ -14,8 +14,7 @@ struct arl2_attn {
   bool half = false;
   int device = 0, sms = 0;
   float* records = nullptr;        // partial records of shared tiles, two per CTA
-  unsigned int* counters = nullptr;   // arrivals per tile, 0 between calls
-  size_t ncounters = 0;
+  float* dq_records = nullptr;     // the dq kernel's
   float* stats = nullptr;          // backward: row statistics
   unsigned int* err = nullptr;
   unsigned long long timeout_ns = 1000000000ull;
@@ -86,6 +85,22 @@ bool tensor_map(CUtensorMap* m, const arl2_tensor* t, int B, int T, int heads, i
                                   heads > 1 ? t->stride[2] : d);
 }
 
+// Whether the split may give parts of a tile to several CTAs. Without lengths and frames every tile
+// has the same units, and the ranges' starts tell; otherwise only the device knows.
+bool cuts_tiles(long long ntiles, long long units, int grid) {
+  const long long total = ntiles * units, ctas = arl2::split_ctas(ntiles, total, grid);
+  for (long long i = 1; i < ctas; ++i)
+    if (i * total / ctas % units != 0) return true;
+  return false;
+}
+bool shares_tiles(const arl2_attn* c, const arl2_attn_shape* s, bool forward) {
+  if (s->q_len || s->k_len || s->frame_len) return true;
+  const long long qt = tiles(s->Tq, 128), kt = tiles(s->Tk, 128), bh = static_cast<long long>(c->B) * c->H;
+  if (forward) return cuts_tiles(bh * tiles(s->Tq, 256), kt, c->sms);
+  return cuts_tiles(bh * qt, kt, c->sms) ||
+         cuts_tiles(static_cast<long long>(c->B) * c->Hkv * kt, qt * (c->H / c->Hkv), c->sms);
+}
+
 arl2::AttnOut out_of(const arl2_tensor* t) {
   return {static_cast<uint16_t*>(t->ptr), t->stride[0], t->stride[1], t->stride[2]};
 }
@@ -99,7 +114,7 @@ arl2::AttnArgs args_of(const arl2_attn* c, const arl2_attn_shape* s) {
   a.scale = s->scale > 0.f ? s->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->d)));
   a.stats = c->stats;
   a.records = c->records;
-  a.counters = c->counters;
+  a.dq_records = c->dq_records;
   a.err = c->err;
   a.timeout_ns = c->timeout_ns;
   return a;
@@ -137,12 +152,9 @@ arl2_status arl2_attn_create(int B, int H, int H_kv, int max_Tq, int max_Tk, int
   c->half = dtype == ARL2_FP16;
   c->device = dev, c->sms = sms;
   const size_t bh = static_cast<size_t>(B) * H;
-  // Two counters per tile, of the kernel that has most.
-  c->ncounters = 2 * std::max(bh * tiles(max_Tq, 128), static_cast<size_t>(B) * H_kv * tiles(max_Tk, 128));
   const bool ok = alloc(&c->records, 2 * static_cast<size_t>(sms) * arl2::attn_record_floats(d), &c->bytes) &&
-                  alloc(&c->counters, c->ncounters, &c->bytes) &&
+                  alloc(&c->dq_records, 2 * static_cast<size_t>(sms) * arl2::attn_dq_record_floats(d), &c->bytes) &&
                   alloc(&c->stats, bh * 2 * tiles(max_Tq, 128) * 128, &c->bytes) && alloc(&c->err, 1, &c->bytes) &&
-                  cudaMemset(c->counters, 0, c->ncounters * sizeof(unsigned int)) == cudaSuccess &&
                   cudaMemset(c->err, 0, sizeof(unsigned int)) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     arl2_attn_destroy(c);
@@ -170,7 +182,8 @@ arl2_status arl2_attn_forward(arl2_attn* c, const arl2_attn_fwd* f, arl2_stream 
   arl2::AttnArgs a = args_of(c, s);
   a.o = out_of(&f->o);
   a.lse = f->lse;
-  return arl2::launch_attn_fwd(c->d, c->half, q, k, v, a, c->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return arl2::launch_attn_fwd(c->d, c->half, q, k, v, a, c->sms, shares_tiles(c, s, true),
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ARL2_OK
              : ARL2_ERR_CUDA;
 }
@@ -192,7 +205,6 @@ arl2_status arl2_attn_backward(arl2_attn* c, const arl2_attn_bwd* f, arl2_stream
   if (!tensor_map(&q, &f->q, c->B, s->Tq, c->H, c->d) || !tensor_map(&k, &f->k, c->B, s->Tk, c->Hkv, c->d) ||
       !tensor_map(&v, &f->v, c->B, s->Tk, c->Hkv, c->d) || !tensor_map(&g, &f->d_o, c->B, s->Tq, c->H, c->d))
     return ARL2_ERR_CUDA;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
   arl2::AttnPrepArgs p{};
   p.o = static_cast<const uint16_t*>(f->o.ptr);
   p.g = static_cast<const uint16_t*>(f->d_o.ptr);
@@ -202,13 +214,14 @@ arl2_status arl2_attn_backward(arl2_attn* c, const arl2_attn_bwd* f, arl2_stream
   p.stats = c->stats;
   p.q_len = s->q_len;
   p.B = c->B, p.H = c->H, p.Tq = s->Tq, p.d = c->d;
-  if (arl2::launch_attn_prep(c->half, p, cs) != cudaSuccess) return ARL2_ERR_CUDA;
   arl2::AttnArgs a = args_of(c, s);
+  a.o = out_of(&f->dq);
   a.dk = out_of(&f->dk);
   a.dv = out_of(&f->dv);
-  if (arl2::launch_attn_dkv(c->d, c->half, q, k, v, g, a, c->sms, cs) != cudaSuccess) return ARL2_ERR_CUDA;
-  a.o = out_of(&f->dq);
-  return arl2::launch_attn_dq(c->d, c->half, q, k, v, g, a, c->sms, cs) == cudaSuccess ? ARL2_OK : ARL2_ERR_CUDA;
+  return arl2::launch_attn_bwd(c->d, c->half, q, k, v, g, p, a, c->sms, shares_tiles(c, s, false),
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ARL2_OK
+             : ARL2_ERR_CUDA;
 }
 
 arl2_status arl2_attn_get_status(arl2_attn* c) {
@@ -217,11 +230,7 @@ arl2_status arl2_attn_get_status(arl2_attn* c) {
   unsigned int h = 0;
   if (cudaMemcpy(&h, c->err, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return ARL2_ERR_CUDA;
   if (h == 0) return ARL2_OK;
-  // An abandoned call may have left counts behind.
-  if (cudaMemset(c->err, 0, sizeof(h)) != cudaSuccess ||
-      cudaMemset(c->counters, 0, c->ncounters * sizeof(unsigned int)) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess)
-    return ARL2_ERR_CUDA;
+  if (cudaMemset(c->err, 0, sizeof(h)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return ARL2_ERR_CUDA;
   return ARL2_ERR_TIMEOUT;
 }
 
@@ -230,7 +239,7 @@ size_t arl2_attn_memory_bytes(const arl2_attn* c) { return c ? c->bytes : 0; }
 void arl2_attn_destroy(arl2_attn* c) {
   if (!c) return;
   cudaFree(c->records);
-  cudaFree(c->counters);
+  cudaFree(c->dq_records);
   cudaFree(c->stats);
   cudaFree(c->err);
   delete c;

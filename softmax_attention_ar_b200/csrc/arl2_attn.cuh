@@ -10,9 +10,8 @@
 // visible (query tile, key tile) pairs, at least one (an empty tile still writes its zeros).
 // The units of all tiles, in order, are cut into equal contiguous ranges, one per CTA, so that
 // every SM gets the same work whatever the lengths and masks are. A tile whose units fall to
-// several CTAs is a sum of partial records in the workspace: the CTA that arrives last (an
-// atomic counter, which it sets back to 0) adds them in the order of the CTAs, so the result
-// does not depend on who it is. No CTA waits for another.
+// several CTAs is a sum of partial records in the workspace: a launch that follows adds them in
+// the order of the CTAs, so the result does not depend on timing. No CTA waits for another.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -96,8 +95,19 @@ __device__ long long head_units(const AttnMask& m, int b, int group) {
   return s;
 }
 
+// The number of CTAs that get a range. Few units per CTA cost more in adding up records than they
+// save: at least kMinUnits each, unless the tiles alone are more.
+constexpr int kMinUnits = 4;
+__host__ __device__ inline long long split_ctas(long long tiles, long long total, long long grid) {
+  long long n = total / kMinUnits;
+  n = n > tiles ? n : tiles;
+  n = n < total ? n : total;
+  n = n < grid ? n : grid;
+  return n > 1 ? n : 1;
+}
+
 template <typename Tiles>
-__device__ void make_split(const AttnMask& m, int B, int heads, int group, int min_units, Split* out) {
+__device__ void make_split(const AttnMask& m, int B, int heads, int group, int c, int grid, Split* out) {
   const int lane = threadIdx.x & 31;
   const bool ragged = m.q_len || m.k_len;
   long long total = 0, per_head = 0;
@@ -107,12 +117,7 @@ __device__ void make_split(const AttnMask& m, int B, int heads, int group, int m
   } else {
     for (int b = 0; b < B; ++b) total += head_units<Tiles>(m, b, group) * heads;
   }
-  // Few units per CTA cost more in merging than they save: at least min_units each, unless the
-  // tiles alone are more.
-  const long long tiles = static_cast<long long>(Tiles::count(m)) * heads * B;
-  long long ctas = max(tiles, total / min_units);
-  ctas = max(1ll, min(min(ctas, total), static_cast<long long>(gridDim.x)));
-  const int c = blockIdx.x;
+  const long long ctas = split_ctas(static_cast<long long>(Tiles::count(m)) * heads * B, total, grid);
   Split s{};
   s.ctas = static_cast<int>(ctas);
   s.total = total;
@@ -172,16 +177,16 @@ struct Seg {
   int units;         // the tile's units (0: nothing is visible, one unit stands for writing zeros)
   int ql, kl;
   long long first;   // global index of the tile's first unit
-  bool whole, range_start;
+  bool whole;
 };
 template <typename Tiles>
 struct Walk {
   const AttnMask& m;
   int heads, group, ntiles;
-  long long u, u0, u1;
+  long long u, u1;
   int b, h, tile, off;
   __device__ Walk(const AttnMask& mask, const Split& s, int heads_, int group_)
-      : m(mask), heads(heads_), group(group_), ntiles(Tiles::count(mask)), u(s.u0), u0(s.u0), u1(s.u1), b(s.b), h(s.h),
+      : m(mask), heads(heads_), group(group_), ntiles(Tiles::count(mask)), u(s.u0), u1(s.u1), b(s.b), h(s.h),
         tile(s.tile), off(s.off) {}
   __device__ bool next(Seg& g) {
     if (u >= u1) return false;
@@ -196,7 +201,6 @@ struct Walk {
     g.ke = static_cast<int>(min(static_cast<long long>(w), off + (u1 - u)));
     g.first = u - off;
     g.whole = g.kb == 0 && g.ke == w;
-    g.range_start = u == u0;
     u += g.ke - g.kb;
     off = 0;
     if (++tile == ntiles) {
@@ -228,6 +232,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   } else {
     return pack_bf16x2(lo, hi);
   }
+}
+// 2^x for a pair on the FMA pipe with paired fp32 operations, max relative error 2.7e-6 for x in
+// [-125, 64] (at least 2^-126 below; a NaN gives a large value). Method as exp2_poly in
+// arl2_device.cuh: x = n + f with n = round(x), then a degree-4 polynomial for 2^f with
+// equioscillating relative error (fit_exp2_poly.py) and n added to the exponent field.
+__device__ __forceinline__ float2 exp2_poly4(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 t = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
+  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+  float2 p = __ffma2_rn(make_float2(0.0095701022f, 0.0095701022f), f, make_float2(0.0559178591f, 0.0559178591f));
+  p = __ffma2_rn(p, f, make_float2(0.2402474433f, 0.2402474433f));
+  p = __ffma2_rn(p, f, make_float2(0.6931217909f, 0.6931217909f));
+  p = __ffma2_rn(p, f, make_float2(0.9999992847f, 0.9999992847f));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+// Column pairs, of every 8, that take it; the others go to the MUFU unit.
+__host__ __device__ constexpr bool fma_pair(uint32_t pairs, int j) { return (pairs >> (j & 7)) & 1u; }
+__device__ __forceinline__ float2 exp2_pair(float2 x, bool on_fma) {
+  return on_fma ? exp2_poly4(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
+}
+// Three-input maximum that keeps a NaN.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // kind::f16 instruction descriptor for fp16 or bf16 operands (both of one type).
 template <bool kHalf>
@@ -319,14 +351,6 @@ __device__ __forceinline__ void regs_dec() {
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-// Rendezvous of a group of warps with a bounded wait (no hang if a warp gave up).
-__device__ __forceinline__ bool warps_sync(uint32_t bar, uint32_t& phase, const Guard& g) {
-  warp_arrive(bar);
-  const bool ok = mbar_wait_warp(bar, phase & 1, g);
-  ++phase;
-  return ok;
 }
 
 }  // namespace

@@ -4,12 +4,13 @@
 // over the visible pairs (arl2_attn.cuh). lse comes from the forward call, so P needs no second
 // pass over the keys.
 //
-// The tensor cores bound it. Three launches:
-//   - arl2_attn_prep_kernel: delta, and lse in log2 units (+inf where a row sees nothing or lies
-//     behind its length: P is then 0 without further tests), padded to whole 128-row tiles;
+// The tensor cores bound it. Launches, each a programmatic dependent of the one before:
+//   - arl2_attn_prep_kernel: -delta, and -lse in log2 units (-inf where a row sees nothing or lies
+//     behind its length: P is then 0 or next to it), padded to whole 128-row tiles;
 //   - arl2_attn_dkv_kernel: a tile is 128 keys of one key head; it runs over the query tiles of
 //     every query head that shares the head, so the heads' sum stays in the accumulators;
-//   - arl2_attn_dq_kernel: a tile is 128 query rows of one head; it runs over the key tiles.
+//   - arl2_attn_dq_kernel: a tile is 128 query rows of one head; it runs over the key tiles;
+//   - arl2_attn_bwd_combine_kernel: adds up the records of tiles shared between CTAs.
 // S and dP are computed in both, 7 products a tile pair instead of the 5 of a single pass. In
 // return no dq leaves the SM before it is complete: a single pass would add 64 KiB of fp32 per
 // tile pair to memory, with atomics whose order changes the result or an ordering that stalls,
@@ -30,11 +31,11 @@ namespace {
 
 constexpr int kBwdThreads = 384;
 constexpr uint32_t kBCtl = 512;   // barriers, split, flags
+constexpr uint32_t kBwdFmaPairs = 0xA4u;   // exponentials on the FMA pipe: pairs 2, 5, 7 of 8
 struct Ctl {                      // after the barriers, at ctl + 320
   Split split;
   uint32_t tmem;
   int abort;
-  int last[2];
 };
 static_assert(sizeof(Ctl) <= 192, "control block");
 template <int D>
@@ -52,16 +53,11 @@ __device__ __forceinline__ void store32(uint16_t* dst, const float (&x)[32]) {
                    pack2<kHalf>(x[c + 6], x[c + 7]));
 }
 
-// Write kCols accumulator columns of this thread's row to an output, times scale: straight when
-// the segment is the whole tile; otherwise as one of the tile's records, which the group of 4
-// warps that arrives last adds up in the order of the CTAs. rec_off: this group's place in a
-// record, [kCols / 4][128] float4. Returns false when a wait ran out.
+// Write kCols accumulator columns of this thread's row: to the output, times scale, when the
+// segment is the whole tile, otherwise to this group's place in a record, [kCols / 4][128] float4.
 template <int kCols, bool kHalf>
-__device__ bool write_rows(const AttnArgs& a, const Split& sp, const Seg& sg, uint32_t acc, int r, bool inside,
-                           bool zero, uint16_t* dst, float scale, size_t rec_floats, size_t rec_off,
-                           unsigned int* counter, uint32_t group_bar, uint32_t& group_phase, uint32_t empty_bar,
-                           int* last_flag, const Guard& g) {
-  float* rec = a.records + record_slot(sp, static_cast<int>(blockIdx.x), sg.first) * rec_floats + rec_off;
+__device__ __forceinline__ void write_rows(const Seg& sg, uint32_t acc, int r, bool inside, bool zero, uint16_t* dst,
+                                           float scale, float* rec, uint32_t empty_bar) {
 #pragma unroll 1
   for (int k = 0; k < kCols; k += 32) {
     uint32_t x[32];
@@ -81,43 +77,32 @@ __device__ bool write_rows(const AttnArgs& a, const Split& sp, const Seg& sg, ui
   }
   tc_fence_before();
   warp_arrive(empty_bar);
-  if (sg.whole) return true;
-  __threadfence();
-  if (!warps_sync(group_bar, group_phase, g)) return false;
-  const int c0 = unit_owner(sp, sg.first), c1 = unit_owner(sp, sg.first + sg.units - 1);
-  if (r == 0) {
-    const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c1 - c0);
-    if (last) *counter = 0;
-    *static_cast<volatile int*>(last_flag) = last;
-  }
-  if (!warps_sync(group_bar, group_phase, g)) return false;
-  if (!*static_cast<volatile int*>(last_flag)) return true;
-  __threadfence();
-#pragma unroll 1
-  for (int k = 0; k < kCols; k += 32) {
-    float y[32] = {};
-    for (int j = c0; j <= c1; ++j) {
-      const float4* oj =
-          reinterpret_cast<const float4*>(a.records + record_slot(sp, j, sg.first) * rec_floats + rec_off);
+}
+// Sum of the records' 32 columns from quad q0 on, row r, over the CTAs c0..c1 in order.
+template <typename Rec>
+__device__ __forceinline__ void add_records(Rec&& record, int c0, int c1, int q0, int r, float (&y)[32]) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 v = __ldcg(oj + (k + e) / 4 * kRows + r);
-        y[e] += v.x;
-        y[e + 1] += v.y;
-        y[e + 2] += v.z;
-        y[e + 3] += v.w;
-      }
+  for (int e = 0; e < 32; ++e) y[e] = 0.f;
+#pragma unroll 4
+  for (int j = c0; j <= c1; ++j) {
+    const float4* x = reinterpret_cast<const float4*>(record(j)) + q0 * kRows + r;
+    float4 v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __ldcg(x + e * kRows);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[4 * e] += v[e].x;
+      y[4 * e + 1] += v[e].y;
+      y[4 * e + 2] += v[e].z;
+      y[4 * e + 3] += v[e].w;
     }
-#pragma unroll
-    for (int e = 0; e < 32; ++e) y[e] = zero ? 0.f : y[e] * scale;
-    if (inside) store32<kHalf>(dst + k, y);
   }
-  return true;
 }
 
 // ------------------------------------------------------------------ prep
 template <bool kHalf>
 __global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_constant__ AttnPrepArgs a) {
+  griddep_launch_dependents();
   const int lanes = a.d / 8;                        // lanes per row, 16 bytes each
   const int Tpad = (a.Tq + kRows - 1) / kRows * kRows;
   const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / lanes;   // (b, t, h), h fastest
@@ -127,7 +112,7 @@ __global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_consta
   const long long bt = row / a.H;
   const int t = static_cast<int>(bt % Tpad), b = static_cast<int>(bt / Tpad);
   const int ql = a.q_len ? min(max(a.q_len[b], 0), a.Tq) : a.Tq;
-  float s = 0.f, l = INFINITY;
+  float s = 0.f, l = -INFINITY;   // both negated: the consumers add them
   if (t < ql) {
     const uint4 ov = *reinterpret_cast<const uint4*>(a.o + b * a.o_sb + t * a.o_st + h * a.o_sh + part * 8);
     const uint4 gv = *reinterpret_cast<const uint4*>(a.g + b * a.g_sb + t * a.g_st + h * a.g_sh + part * 8);
@@ -146,7 +131,7 @@ __global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_consta
       s = fmaf(x.y, y.y, s);
     }
     const float lse = a.lse[(static_cast<size_t>(b) * a.H + h) * a.Tq + t];
-    l = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    l = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
   }
   const int lane = threadIdx.x & 31;
   const unsigned mask = ((1u << lanes) - 1) << (lane / lanes * lanes);   // the row's lanes
@@ -154,7 +139,7 @@ __global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_consta
   if (part == 0) {
     float* out = a.stats + (static_cast<size_t>(b) * a.H + h) * 2 * Tpad + t;
     out[0] = l;
-    out[Tpad] = s;
+    out[Tpad] = -s;
   }
 }
 
@@ -174,8 +159,7 @@ enum : int {
   kKDReady,               // 8 warps
   kKAccFull,
   kKAccEmpty,             // 8 warps
-  kKGroup,                // + group (2), 4 warps
-  kKSide = kKGroup + 2,
+  kKSide,
   kKFinal,                // the MMA warp's commit and 8 warps
   kKBars
 };
@@ -201,7 +185,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKBars; ++i) {
       const bool by8 = i == kKTEmpty || i == kKTEmpty + 1 || i == kKPReady || i == kKDReady || i == kKAccEmpty;
-      mbar_init(bar(i), by8 ? 8 : i == kKGroup || i == kKGroup + 1 ? 4 : i == kKFinal ? 9 : 1);
+      mbar_init(bar(i), by8 ? 8 : i == kKFinal ? 9 : 1);
     }
     shared->abort = 0;
     fence_barrier_init();
@@ -214,7 +198,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       prefetch_tmap(&tm_g);
     }
     __syncwarp();
-    make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, 4, &shared->split);
+    make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, blockIdx.x, gridDim.x, &shared->split);
   }
   if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
   tc_fence_before();
@@ -227,13 +211,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // of the block's 384 x 168.
   if (warp == 0) {
     regs_dec<88>();
-    const Split sp = shared->split;
+    const Split& sp = shared->split;
     Walk<KeyTiles> walk(a.mask, sp, a.Hkv, group);
     Seg sg;
     const bool lead = elect_one();
     const int Tpad = (a.mask.Tq + kRows - 1) / kRows * kRows;
     uint32_t ns = 0, nq = 0, ng = 0, nt = 0, side_phase = 0;   // copies made
-    bool ok = true;
+    bool ok = true, waited = false;
     while (ok && walk.next(sg)) {
       if (sg.units == 0) continue;
       if (ns > 0 && !mbar_wait_warp(bar(kKKVEmpty), (ns - 1) & 1, g)) break;
@@ -255,6 +239,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         ok = nt < 2 || mbar_wait_warp(bar(kKTEmpty + nt % 2), (nt / 2 - 1) & 1, g);
         if (!ok) break;
+        if (!waited) {   // the statistics come from the launch before this one
+          griddep_wait();
+          griddep_launch_dependents();
+          waited = true;
+        }
         if (lead) {
           const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + hd) * 2 * Tpad + i * kRows;
           mbar_expect_tx(bar(kKTFull + nt % 2), 1024);
@@ -275,6 +264,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     __syncwarp();
+    if (!waited) griddep_wait();   // this grid ends after the one before it
     // Every copy issued lands before the CTA may exit.
     if (ns > 0) mbar_wait_drain(bar(kKKVFull), (ns - 1) & 1);
     for (uint32_t s = 0; s < 3; ++s)
@@ -285,7 +275,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 1) {
     regs_dec<88>();
-    const Split sp = shared->split;
+    const Split& sp = shared->split;
     Walk<KeyTiles> walk(a.mask, sp, a.Hkv, group);
     Seg sg;
     const bool lead = elect_one();
@@ -370,15 +360,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     regs_dec<88>();
   } else {
     regs_inc<200>();
-    const Split sp = shared->split;
+    const Split& sp = shared->split;
     Walk<KeyTiles> walk(a.mask, sp, a.Hkv, group);
     Seg sg;
     const int wg = (warp >> 2) - 1;                            // columns 64 wg ..; dv (0) or dk (1) at the end
     const int r = (warp & 3) * 32 + (threadIdx.x & 31);        // key row == TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
     const uint32_t s_col = c_s + lanes + 64u * wg, dp_col = c_dp + lanes + 64u * wg;
-    const float to_log2 = a.scale * 1.4426950408889634f;
-    uint32_t n = 0, ns = 0, group_phase = 0;
+    const float2 sc = make_float2(a.scale * 1.4426950408889634f, a.scale * 1.4426950408889634f);
+    uint32_t n = 0, ns = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
       const int j = sg.tile * kRows + r;
@@ -400,7 +390,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         const float4* st = reinterpret_cast<const float4*>(attn_smem + 7 * TO::kBytes + n % 2 * 1024) + 16 * wg;
         const int hidden = row0 - (i * kRows + 64 * wg);   // this thread's columns below it see nothing
-        float p[64];
+        float2 p[32];
         {
           uint32_t s[2][32];
           tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
@@ -408,21 +398,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int k = 0; k < 64; k += 4) {
             const float4 l = st[k / 4];
             const uint32_t* x = &s[k >> 5][k & 31];
-            p[k] = ex2_approx(fmaf(__uint_as_float(x[0]), to_log2, -l.x));
-            p[k + 1] = ex2_approx(fmaf(__uint_as_float(x[1]), to_log2, -l.y));
-            p[k + 2] = ex2_approx(fmaf(__uint_as_float(x[2]), to_log2, -l.z));
-            p[k + 3] = ex2_approx(fmaf(__uint_as_float(x[3]), to_log2, -l.w));
+            const float2 x0 = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+            const float2 x1 = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+            p[k / 2] = exp2_pair(__ffma2_rn(x0, sc, make_float2(l.x, l.y)), fma_pair(kBwdFmaPairs, k / 2));
+            p[k / 2 + 1] = exp2_pair(__ffma2_rn(x1, sc, make_float2(l.z, l.w)), fma_pair(kBwdFmaPairs, k / 2 + 1));
           }
         }
         if (__any_sync(0xffffffffu, hidden > 0)) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k < hidden) p[k] = 0.f;
+          for (int k = 0; k < 64; k += 2) {
+            if (k < hidden) p[k / 2].x = 0.f;
+            if (k + 1 < hidden) p[k / 2].y = 0.f;
+          }
         }
         {
           uint32_t w[32];
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) w[k / 2] = pack2<kHalf>(p[k], p[k + 1]);
+          for (int k = 0; k < 32; ++k) w[k] = pack2<kHalf>(p[k].x, p[k].y);
           tmem_st32(s_col, w);
         }
         tmem_wait_st();
@@ -438,9 +430,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int k = 0; k < 64; k += 4) {
             const float4 e = st[32 + k / 4];
             const uint32_t* x = &d[k >> 5][k & 31];
-            w[k / 2] = pack2<kHalf>(p[k] * (__uint_as_float(x[0]) - e.x), p[k + 1] * (__uint_as_float(x[1]) - e.y));
-            w[k / 2 + 1] =
-                pack2<kHalf>(p[k + 2] * (__uint_as_float(x[2]) - e.z), p[k + 3] * (__uint_as_float(x[3]) - e.w));
+            const float2 d0 = __fmul2_rn(
+                p[k / 2], __fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(e.x, e.y)));
+            const float2 d1 = __fmul2_rn(
+                p[k / 2 + 1], __fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(e.z, e.w)));
+            w[k / 2] = pack2<kHalf>(d0.x, d0.y);
+            w[k / 2 + 1] = pack2<kHalf>(d1.x, d1.y);
           }
           tmem_st32(dp_col, w);
         }
@@ -454,10 +449,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       ++ns;
       tc_fence_after();
-      ok = write_rows<D, kHalf>(a, sp, sg, (wg ? c_dk : c_dv) + lanes, r, inside, j >= sg.kl, dst,
-                                wg ? a.scale : 1.f, attn_record_floats(D), static_cast<size_t>(wg) * D * kRows,
-                                a.counters + ((static_cast<size_t>(sg.b) * a.Hkv + sg.h) * walk.ntiles + sg.tile) * 2 + wg,
-                                bar(kKGroup + wg), group_phase, bar(kKAccEmpty), &shared->last[wg], g);
+      float* rec = a.records + record_slot(sp, blockIdx.x, sg.first) * attn_record_floats(D) + wg * D * kRows;
+      write_rows<D, kHalf>(sg, (wg ? c_dk : c_dv) + lanes, r, inside, j >= sg.kl, dst, wg ? a.scale : 1.f, rec,
+                           bar(kKAccEmpty));
     }
     __syncwarp();
     tc_fence_before();
@@ -485,8 +479,7 @@ enum : int {
   kQDReady,               // 8 warps
   kQAccFull,
   kQAccEmpty,             // 8 warps
-  kQGroup,                // + group (2), 4 warps
-  kQSide = kQGroup + 2,
+  kQSide,
   kQFinal,                // the MMA warp's commit and 8 warps
   kQBars
 };
@@ -510,12 +503,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Guard g{&shared->abort, a.err, a.timeout_ns};
   const int group = a.H / a.Hkv;
 
+  griddep_launch_dependents();   // the combining launch waits for this grid's end before it reads
   if (threadIdx.x == 0) {
     for (int i = 0; i < kQBars; ++i)
-      mbar_init(bar(i), i == kQDReady || i == kQAccEmpty                ? 8
-                        : i == kQGroup || i == kQGroup + 1 ? 4
-                        : i == kQFinal                                 ? 9
-                                                                       : 1);
+      mbar_init(bar(i), i == kQDReady || i == kQAccEmpty ? 8 : i == kQFinal ? 9 : 1);
     shared->abort = 0;
     fence_barrier_init();
   }
@@ -527,7 +518,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       prefetch_tmap(&tm_g);
     }
     __syncwarp();
-    make_split<QTiles>(a.mask, a.B, a.H, 1, 4, &shared->split);
+    make_split<QTiles>(a.mask, a.B, a.H, 1, blockIdx.x, gridDim.x, &shared->split);
   }
   if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
   tc_fence_before();
@@ -537,7 +528,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t c_dp = tmem + 256, c_dq = tmem + 384;   // S buffers at 0 and 128
 
   if (warp == 0) {
-    const Split sp = shared->split;
+    const Split& sp = shared->split;
     Walk<QTiles> walk(a.mask, sp, a.H, 1);
     Seg sg;
     const bool lead = elect_one();
@@ -570,6 +561,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     __syncwarp();
+    griddep_wait();   // this grid ends after the one before it
     // Every copy issued lands before the CTA may exit.
     if (ns > 0) mbar_wait_drain(bar(kQQFull), (ns - 1) & 1);
     for (uint32_t s = 0; s < 3; ++s)
@@ -577,7 +569,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (uint32_t s = 0; s < 2; ++s)
       if (nv > s) mbar_wait_drain(bar(kQVFull + s), ((nv - s + 1) / 2 - 1) & 1);
   } else if (warp == 1) {
-    const Split sp = shared->split;
+    const Split& sp = shared->split;
     Walk<QTiles> walk(a.mask, sp, a.H, 1);
     Seg sg;
     const bool lead = elect_one();
@@ -639,17 +631,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (lead) mma_commit(bar(kQFinal));
     __syncwarp();
   } else if (warp >= 4) {
-    const Split sp = shared->split;
+    const Split& sp = shared->split;
     Walk<QTiles> walk(a.mask, sp, a.H, 1);
     Seg sg;
     constexpr int kCols = D > 32 ? D / 2 : 32;                 // output columns of a group; d = 32: of the first
     const int wg = (warp >> 2) - 1;                            // score columns 64 wg ..
     const int r = (warp & 3) * 32 + (threadIdx.x & 31);        // query row == TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
-    const float to_log2 = a.scale * 1.4426950408889634f;
+    const float2 sc = make_float2(a.scale * 1.4426950408889634f, a.scale * 1.4426950408889634f);
     const int Tpad = (a.mask.Tq + kRows - 1) / kRows * kRows;
     const bool writes = D > 32 || wg == 0;
-    uint32_t n = 0, ns = 0, group_phase = 0;
+    uint32_t n = 0, ns = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
       const int row = sg.tile * kRows + r;
@@ -662,7 +654,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         continue;
       }
       const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + sg.h) * 2 * Tpad + row;
-      const float lse = st[0], delta = st[Tpad];
+      const float2 neg_lse = make_float2(st[0], st[0]), neg_delta = make_float2(st[Tpad], st[Tpad]);
       const int limit = row < sg.ql ? key_limit(a.mask, row, sg.kl) : 0;
       for (int t = sg.kb; t < sg.ke; ++t, ++n) {
         ok = mbar_wait_warp(bar(kQSFull + (n & 1)), (n / 2) & 1, g);
@@ -670,12 +662,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         const uint32_t s_col = tmem + lanes + 128u * (n & 1) + 64u * wg, dp_col = c_dp + lanes + 64u * wg;
         const int seen = limit - (t * kRows + 64 * wg);   // this thread's columns that the row sees
-        float p[64];
+        float2 p[32];
         {
           uint32_t s[2][32];
           tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) p[k] = ex2_approx(fmaf(__uint_as_float(s[k >> 5][k & 31]), to_log2, -lse));
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t* x = &s[k >> 4][2 * (k & 15)];
+            p[k] = exp2_pair(__ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc, neg_lse),
+                             fma_pair(kBwdFmaPairs, k));
+          }
         }
         ok = mbar_wait_warp(bar(kQDFull), n & 1, g);
         if (!ok) break;
@@ -683,14 +679,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint32_t d[2][32], w[32];
         tmem_ld32x2_wait(dp_col, d[0], dp_col + 32, d[1]);
 #pragma unroll
-        for (int k = 0; k < 64; ++k) p[k] *= __uint_as_float(d[k >> 5][k & 31]) - delta;
+        for (int k = 0; k < 32; ++k) {
+          const uint32_t* x = &d[k >> 4][2 * (k & 15)];
+          p[k] = __fmul2_rn(p[k], __fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), neg_delta));
+        }
         if (__any_sync(0xffffffffu, seen < 64)) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k >= seen) p[k] = 0.f;
+          for (int k = 0; k < 64; k += 2) {
+            if (k >= seen) p[k / 2].x = 0.f;
+            if (k + 1 >= seen) p[k / 2].y = 0.f;
+          }
         }
 #pragma unroll
-        for (int k = 0; k < 64; k += 2) w[k / 2] = pack2<kHalf>(p[k], p[k + 1]);
+        for (int k = 0; k < 32; ++k) w[k] = pack2<kHalf>(p[k].x, p[k].y);
         tmem_st32(s_col, w);
         tmem_wait_st();
         tc_fence_before();
@@ -700,11 +701,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       ++ns;
       tc_fence_after();
+      float* rec = a.dq_records + record_slot(sp, blockIdx.x, sg.first) * attn_dq_record_floats(D) + wg * kCols * kRows;
       if (writes)
-        ok = write_rows<kCols, kHalf>(a, sp, sg, c_dq + lanes + kCols * wg, r, inside, row >= sg.ql, dst, a.scale,
-                                      attn_record_floats(D), static_cast<size_t>(wg) * kCols * kRows,
-                                      a.counters + ((static_cast<size_t>(sg.b) * a.H + sg.h) * walk.ntiles + sg.tile) * 2 + wg,
-                                      bar(kQGroup + wg), group_phase, bar(kQAccEmpty), &shared->last[wg], g);
+        write_rows<kCols, kHalf>(sg, c_dq + lanes + kCols * wg, r, inside, row >= sg.ql, dst, a.scale, rec,
+                                 bar(kQAccEmpty));
       else
         warp_arrive(bar(kQAccEmpty));
     }
@@ -721,6 +721,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ records
+// Adds up the records of the tiles shared between CTAs, as the forward's (arl2_attn_fwd.cu): block
+// (c, y) takes 32 columns of the tile at the start of CTA c's range; y < D / 32: of dv, then of
+// dk, then, in the dq kernel's split, of dq.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ Split split;
+  constexpr int kParts = D / 32;
+  const int c = static_cast<int>(blockIdx.x) + 1, r = threadIdx.x, what = blockIdx.y / kParts;
+  const int k0 = 32 * (blockIdx.y % kParts), group = a.H / a.Hkv;
+  if (threadIdx.x < 32) {
+    if (what < 2)
+      make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, c, gridDim.x + 1, &split);
+    else
+      make_split<QTiles>(a.mask, a.B, a.H, 1, c, gridDim.x + 1, &split);
+  }
+  __syncthreads();
+  const Split sp = split;
+  griddep_wait();   // the records; every block, so that this grid ends after the one before it
+  const long long first = sp.u0 - sp.off;
+  if (c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
+  const int ql = q_length(a.mask, sp.b), kl = k_length(a.mask, sp.b);
+  const int units = what < 2 ? KeyTiles::units(a.mask, sp.tile, ql, kl, group) : QTiles::units(a.mask, sp.tile, ql, kl, 1);
+  const int c1 = unit_owner(sp, first + max(1, units) - 1);
+  const int row = sp.tile * kRows + r;
+  float y[32];
+  if (what < 2)
+    add_records([&](int j) { return a.records + record_slot(sp, j, first) * attn_record_floats(D) + what * D * kRows; },
+                c - 1, c1, k0 / 4, r, y);
+  else
+    add_records([&](int j) { return a.dq_records + record_slot(sp, j, first) * attn_dq_record_floats(D); }, c - 1, c1,
+                k0 / 4, r, y);
+  const bool zero = row >= (what < 2 ? kl : ql);
+  const float scale = what == 0 ? 1.f : a.scale;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[e] = zero ? 0.f : y[e] * scale;
+  const AttnOut& out = what == 0 ? a.dv : what == 1 ? a.dk : a.o;
+  if (row < (what < 2 ? a.mask.Tk : a.mask.Tq))
+    store32<kHalf>(out.ptr + sp.b * out.sb + row * out.st + sp.h * out.sh + k0, y);
+}
+
 template <int D, bool kHalf>
 cudaError_t setup() {
   cudaError_t e = cudaFuncSetAttribute(arl2_attn_dkv_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -730,23 +771,17 @@ cudaError_t setup() {
                               static_cast<int>(bwd_smem<D>()));
 }
 template <int D, bool kHalf>
-cudaError_t launch(bool dq, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& g,
-                   const AttnArgs& a, int ctas, cudaStream_t st) {
-  if (dq)
-    arl2_attn_dq_kernel<D, kHalf><<<ctas, kBwdThreads, bwd_smem<D>(), st>>>(q, k, v, g, a);
-  else
-    arl2_attn_dkv_kernel<D, kHalf><<<ctas, kBwdThreads, bwd_smem<D>(), st>>>(q, k, v, g, a);
-  return cudaGetLastError();
-}
-cudaError_t by_type(bool dq, int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                    const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st) {
-  if (half)
-    return d == 32   ? launch<32, true>(dq, q, k, v, g, a, ctas, st)
-           : d == 64 ? launch<64, true>(dq, q, k, v, g, a, ctas, st)
-                     : launch<128, true>(dq, q, k, v, g, a, ctas, st);
-  return d == 32   ? launch<32, false>(dq, q, k, v, g, a, ctas, st)
-         : d == 64 ? launch<64, false>(dq, q, k, v, g, a, ctas, st)
-                   : launch<128, false>(dq, q, k, v, g, a, ctas, st);
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& g,
+                   const AttnPrepArgs& prep, const AttnArgs& a, int ctas, bool combine, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.B) * ((a.mask.Tq + kRows - 1) / kRows * kRows) * a.H;
+  const unsigned blocks = static_cast<unsigned>((rows * (D / 8) + 255) / 256);
+  cudaError_t e = launch_chained(arl2_attn_prep_kernel<kHalf>, dim3(blocks), 256, 0, st, false, prep);
+  if (e == cudaSuccess)
+    e = launch_chained(arl2_attn_dkv_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a);
+  if (e == cudaSuccess)
+    e = launch_chained(arl2_attn_dq_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a);
+  if (e != cudaSuccess || !combine || ctas < 2) return e;
+  return launch_chained(arl2_attn_bwd_combine_kernel<D, kHalf>, dim3(ctas - 1, 3 * (D / 32)), kRows, 0, st, true, a);
 }
 
 }  // namespace
@@ -761,23 +796,16 @@ cudaError_t attn_bwd_setup() {
   return e;
 }
 
-cudaError_t launch_attn_prep(bool half, const AttnPrepArgs& a, cudaStream_t st) {
-  const long long rows = static_cast<long long>(a.B) * ((a.Tq + kRows - 1) / kRows * kRows) * a.H;
-  const long long blocks = (rows * (a.d / 8) + 255) / 256;
+cudaError_t launch_attn_bwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const CUtensorMap& g, const AttnPrepArgs& prep, const AttnArgs& a, int ctas, bool combine,
+                            cudaStream_t st) {
   if (half)
-    arl2_attn_prep_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
-  else
-    arl2_attn_prep_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_attn_dkv(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st) {
-  return by_type(false, d, half, q, k, v, g, a, ctas, st);
-}
-cudaError_t launch_attn_dq(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                           const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st) {
-  return by_type(true, d, half, q, k, v, g, a, ctas, st);
+    return d == 32   ? launch<32, true>(q, k, v, g, prep, a, ctas, combine, st)
+           : d == 64 ? launch<64, true>(q, k, v, g, prep, a, ctas, combine, st)
+                     : launch<128, true>(q, k, v, g, prep, a, ctas, combine, st);
+  return d == 32   ? launch<32, false>(q, k, v, g, prep, a, ctas, combine, st)
+         : d == 64 ? launch<64, false>(q, k, v, g, prep, a, ctas, combine, st)
+                   : launch<128, false>(q, k, v, g, prep, a, ctas, combine, st);
 }
 
 }  // namespace arl2

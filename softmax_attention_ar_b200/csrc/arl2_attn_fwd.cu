@@ -39,8 +39,7 @@ enum : int {
   kFPReady = kFSFull + 2,
   kFOFull = kFPReady + 2,
   kFOEmpty = kFOFull + 2,
-  kFGroup = kFOEmpty + 2,
-  kFSide = kFGroup + 2,
+  kFSide = kFOEmpty + 2,
   kFFinal = kFSide + 1,
   kFBars = kFFinal + 1
 };
@@ -52,6 +51,7 @@ constexpr uint32_t fwd_smem() {
 }
 static_assert(fwd_smem<128>() <= 232448, "shared memory per CTA");
 constexpr float kRaise = 8.0f;    // log2 units
+constexpr uint32_t kFwdFmaPairs = 0xA4u;   // exponentials on the FMA pipe: pairs 2, 5, 7 of 8
 
 // Per record: [2 query tiles][d / 4 quads][128 rows] float4 of O, then [2][2][128] m and l.
 template <int D>
@@ -83,13 +83,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   Split* split = reinterpret_cast<Split*>(gctl + 256);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gctl + 256 + sizeof(Split));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
   const int warp = threadIdx.x >> 5;
   const Guard g{abort_flag, a.err, a.timeout_ns};
 
+  griddep_launch_dependents();   // the combining launch waits for this grid's end before it reads
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFBars; ++i) {
-      const bool by4 = (i >= kFPReady && i < kFPReady + 2) || (i >= kFOEmpty && i < kFGroup + 2);
+      const bool by4 = (i >= kFPReady && i < kFPReady + 2) || (i >= kFOEmpty && i < kFOEmpty + 2);
       mbar_init(bar(i), i == kFFinal ? 9 : by4 ? 4 : 1);
     }
     *abort_flag = 0;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       prefetch_tmap(&tm_v);
     }
     __syncwarp();
-    make_split<FwdTiles>(a.mask, a.B, a.H, 1, 4, split);
+    make_split<FwdTiles>(a.mask, a.B, a.H, 1, blockIdx.x, gridDim.x, split);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
@@ -110,13 +110,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // Registers move from the copy and MMA warps to the softmax, which holds a row of 128 scores:
-  // 128 threads x 72 + 256 x 208 = 62464 of the block's 384 x 168.
+  // 128 threads x 72 + 256 x 216 = 64512, the block's 384 x 168.
   const int group = a.H / a.Hkv;
   const uint32_t q_tile = base, ring0 = base + 2 * TO::kBytes;
 
   if (warp == 0) {
     regs_dec<72>();
-    const Split sp = *split;
+    const Split& sp = *split;
     Walk<FwdTiles> walk(a.mask, sp, a.H, 1);
     Seg sg;
     const bool lead = elect_one();
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
   } else if (warp == 1) {
     regs_dec<72>();
-    const Split sp = *split;
+    const Split& sp = *split;
     Walk<FwdTiles> walk(a.mask, sp, a.H, 1);
     Seg sg;
     const bool lead = elect_one();
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   } else if (warp < 4) {
     regs_dec<72>();
   } else {
-    regs_inc<208>();
-    const Split sp = *split;
+    regs_inc<216>();
+    const Split& sp = *split;
     Walk<FwdTiles> walk(a.mask, sp, a.H, 1);
     Seg sg;
     const int i = (warp >> 2) - 1;                              // query tile
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
     const uint32_t s_col = tmem + lanes + 128u * i, o_col = tmem + lanes + 256u + 128u * i;
     const float to_log2 = a.scale * 1.4426950408889634f;
-    uint32_t nt = 0, nseg = 0, group_phase = 0;
+    uint32_t nt = 0, nseg = 0;
     const int c = static_cast<int>(blockIdx.x);
     bool ok = true;
     while (ok && walk.next(sg)) {
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
         tmem_ld32x2_wait(s_col + 64, s[2], s_col + 96, s[3]);
         const int seen = limit - t * kRows;   // columns of this tile that the row sees
-        if (__any_sync(0xffffffffu, seen < kRows)) {
+        const bool masked = __any_sync(0xffffffffu, seen < kRows);
+        if (masked) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -271,11 +272,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float top[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          top[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+          top[q] = __uint_as_float(s[q][0]);
 #pragma unroll
-          for (int k = 2; k < 32; k += 2) top[q] = fmax3(top[q], __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
+          for (int k = 1; k < 31; k += 2)
+            top[q] = fmax3_nan(top[q], __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
         }
-        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * to_log2;
+        top[0] = fmax3_nan(top[0], __uint_as_float(s[0][31]), __uint_as_float(s[1][31]));
+        top[1] = fmax3_nan(top[1], __uint_as_float(s[2][31]), __uint_as_float(s[3][31]));
+        const float tile_top = fmax3_nan(fmax3_nan(top[0], top[1], top[2]), top[3], top[3]) * to_log2;
         const bool raise = tile_top > m + kRaise || (m == -INFINITY && tile_top > m);
         if (__any_sync(0xffffffffu, raise)) {
           const float m_new = raise ? tile_top : m;
@@ -294,20 +298,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
         const float shift = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sc = make_float2(to_log2, to_log2), sh = make_float2(-shift, -shift);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          float2 e[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            e[k] = exp2_pair(
+                __ffma2_rn(make_float2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), sc, sh),
+                fma_pair(kFwdFmaPairs, k));
+          if (masked) {   // exactly 0, where the FMA pipe's 2^-inf is only next to it
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              if (32 * q + 2 * k >= seen) e[k].x = 0.f;
+              if (32 * q + 2 * k + 1 >= seen) e[k].y = 0.f;
+            }
+          }
           uint32_t p[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(s[q][k]), to_log2, -shift));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(s[q][k + 1]), to_log2, -shift));
-            sum[(k >> 1) & 3] += p0 + p1;
-            p[k >> 1] = pack2<kHalf>(p0, p1);
+          for (int k = 0; k < 16; ++k) {
+            sum[k & 1] = __fadd2_rn(sum[k & 1], e[k]);
+            p[k] = pack2<kHalf>(e[k].x, e[k].y);
           }
           tmem_st16(s_col + 16 * q, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum[0] = __fadd2_rn(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+        if (!(tile_top < INFINITY)) l = NAN;   // a NaN or +inf among the scores: the row has no softmax
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar(kFPReady + i));
@@ -332,7 +350,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (row < a.mask.Tq) lse[row] = in_q && limit > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         continue;
       }
-      // A part of the tile: its record, then the last to arrive adds them up.
+      // A part of the tile: its record.
       float* rec = fwd_record<D>(a, record_slot(sp, c, sg.first));
       float4* ro = reinterpret_cast<float4*>(rec) + i * (D / 4) * kRows;
       float* rml = rec + 2 * kRows * D + i * 2 * kRows;
@@ -349,57 +367,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       warp_arrive(bar(kFOEmpty + i));
       rml[r] = m;
       rml[kRows + r] = l;
-      __threadfence();
-      ok = warps_sync(bar(kFGroup + i), group_phase, g);
-      if (!ok) break;
-      const int c0 = unit_owner(sp, sg.first), c1 = unit_owner(sp, sg.first + sg.units - 1);
-      unsigned int* counter =
-          a.counters + ((static_cast<size_t>(sg.b) * a.H + sg.h) * walk.ntiles + sg.tile) * 2 + i;
-      if (r == 0) {
-        const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c1 - c0);
-        if (last) *counter = 0;
-        last_flag[i] = last;
-      }
-      ok = warps_sync(bar(kFGroup + i), group_phase, g);
-      if (!ok) break;
-      if (!last_flag[i]) continue;
-      __threadfence();
-      float m_all = -INFINITY, l_all = 0.f;
-      for (int j = c0; j <= c1; ++j) {
-        const float* ml = fwd_record<D>(a, record_slot(sp, j, sg.first)) + 2 * kRows * D + i * 2 * kRows;
-        const float mj = __ldcg(ml + r), lj = __ldcg(ml + kRows + r);
-        if (mj > m_all) {
-          l_all = m_all == -INFINITY ? lj : fmaf(l_all, exp2f(m_all - mj), lj);
-          m_all = mj;
-        } else {
-          l_all += mj == -INFINITY ? lj : lj * exp2f(mj - m_all);
-        }
-      }
-      const float f = l_all > 0.f || l_all != l_all ? 1.f / l_all : 0.f;
-#pragma unroll 1
-      for (int k = 0; k < D; k += 32) {
-        float y[32] = {};
-        for (int j = c0; j <= c1; ++j) {
-          const float* rj = fwd_record<D>(a, record_slot(sp, j, sg.first));
-          const float4* oj = reinterpret_cast<const float4*>(rj) + i * (D / 4) * kRows;
-          const float mj = __ldcg(rj + 2 * kRows * D + i * 2 * kRows + r);
-          const float w = mj == -INFINITY ? 0.f : exp2f(mj - m_all) * f;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 v = __ldcg(oj + (k + e) / 4 * kRows + r);
-            y[e] = fmaf(v.x, w, y[e]);
-            y[e + 1] = fmaf(v.y, w, y[e + 1]);
-            y[e + 2] = fmaf(v.z, w, y[e + 2]);
-            y[e + 3] = fmaf(v.w, w, y[e + 3]);
-          }
-        }
-        if (!(in_q && limit > 0)) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = 0.f;
-        }
-        if (row < a.mask.Tq) store_row<D, kHalf>(a, sg.b, sg.h, row, y, k);
-      }
-      if (row < a.mask.Tq) lse[row] = in_q && limit > 0 ? (m_all + log2f(l_all)) * 0.6931471805599453f : -INFINITY;
     }
     __syncwarp();
     tc_fence_before();
@@ -414,6 +381,58 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
+// Adds up the records of the tiles shared between CTAs, in the order of the CTAs. Block (c, y)
+// takes the tile at the start of CTA c's range, if it is the second to hold a part of it; y is
+// one of its two query tiles and 32 of its columns. Thread = row.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ Split split;
+  const int c = static_cast<int>(blockIdx.x) + 1, r = threadIdx.x;
+  if (threadIdx.x < 32) make_split<FwdTiles>(a.mask, a.B, a.H, 1, c, gridDim.x + 1, &split);
+  __syncthreads();
+  const Split sp = split;
+  griddep_wait();   // the records; every block, so that this grid ends after the one before it
+  const long long first = sp.u0 - sp.off;
+  if (c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
+  const int i = blockIdx.y & 1, k0 = 32 * (blockIdx.y >> 1);
+  const int ql = q_length(a.mask, sp.b), kl = k_length(a.mask, sp.b);
+  const int row = sp.tile * kFwdRows + i * kRows + r;
+  if (sp.tile * kFwdRows + i * kRows >= ql) return;   // written by the forward kernel
+  const int units = max(1, FwdTiles::units(a.mask, sp.tile, ql, kl, 1));
+  const int c1 = unit_owner(sp, first + units - 1);
+  const bool sees = row < ql && key_limit(a.mask, row, kl) > 0;
+  float m = -INFINITY;
+  for (int j = c - 1; j <= c1; ++j)
+    m = fmaxf(m, __ldcg(fwd_record<D>(a, record_slot(sp, j, first)) + 2 * kRows * D + i * 2 * kRows + r));
+  float l = 0.f, y[32] = {};
+#pragma unroll 2
+  for (int j = c - 1; j <= c1; ++j) {
+    const float* rec = fwd_record<D>(a, record_slot(sp, j, first));
+    const float4* o = reinterpret_cast<const float4*>(rec) + (i * (D / 4) + k0 / 4) * kRows + r;
+    const float* ml = rec + 2 * kRows * D + i * 2 * kRows + r;
+    float4 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __ldcg(o + e * kRows);
+    const float mj = __ldcg(ml), w = mj == -INFINITY ? 0.f : exp2f(mj - m);
+    l = fmaf(__ldcg(ml + kRows), w, l);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[4 * e] = fmaf(x[e].x, w, y[4 * e]);
+      y[4 * e + 1] = fmaf(x[e].y, w, y[4 * e + 1]);
+      y[4 * e + 2] = fmaf(x[e].z, w, y[4 * e + 2]);
+      y[4 * e + 3] = fmaf(x[e].w, w, y[4 * e + 3]);
+    }
+  }
+  if (row >= a.mask.Tq) return;
+  const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[e] = sees ? y[e] * f : 0.f;
+  store_row<D, kHalf>(a, sp.b, sp.h, row, y, k0);
+  if (k0 == 0)
+    a.lse[(static_cast<size_t>(sp.b) * a.H + sp.h) * a.mask.Tq + row] =
+        sees ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 template <int D, bool kHalf>
 cudaError_t setup() {
   return cudaFuncSetAttribute(arl2_attn_fwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -421,9 +440,11 @@ cudaError_t setup() {
 }
 template <int D, bool kHalf>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas,
-                   cudaStream_t st) {
-  arl2_attn_fwd_kernel<D, kHalf><<<ctas, kFwdThreads, fwd_smem<D>(), st>>>(q, k, v, a);
-  return cudaGetLastError();
+                   bool combine, cudaStream_t st) {
+  const cudaError_t e =
+      launch_chained(arl2_attn_fwd_kernel<D, kHalf>, dim3(ctas), kFwdThreads, fwd_smem<D>(), st, false, q, k, v, a);
+  if (e != cudaSuccess || !combine || ctas < 2) return e;
+  return launch_chained(arl2_attn_fwd_combine_kernel<D, kHalf>, dim3(ctas - 1, 2 * (D / 32)), kRows, 0, st, true, a);
 }
 
 }  // namespace
@@ -439,12 +460,12 @@ cudaError_t attn_fwd_setup() {
 }
 
 cudaError_t launch_attn_fwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const AttnArgs& a, int ctas, cudaStream_t st) {
+                            const AttnArgs& a, int ctas, bool combine, cudaStream_t st) {
   if (half)
-    return d == 32 ? launch<32, true>(q, k, v, a, ctas, st)
-                   : d == 64 ? launch<64, true>(q, k, v, a, ctas, st) : launch<128, true>(q, k, v, a, ctas, st);
-  return d == 32 ? launch<32, false>(q, k, v, a, ctas, st)
-                 : d == 64 ? launch<64, false>(q, k, v, a, ctas, st) : launch<128, false>(q, k, v, a, ctas, st);
+    return d == 32 ? launch<32, true>(q, k, v, a, ctas, combine, st)
+                   : d == 64 ? launch<64, true>(q, k, v, a, ctas, combine, st) : launch<128, true>(q, k, v, a, ctas, combine, st);
+  return d == 32 ? launch<32, false>(q, k, v, a, ctas, combine, st)
+                 : d == 64 ? launch<64, false>(q, k, v, a, ctas, combine, st) : launch<128, false>(q, k, v, a, ctas, combine, st);
 }
 
 }  // namespace arl2

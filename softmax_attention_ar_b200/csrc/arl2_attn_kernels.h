@@ -22,9 +22,9 @@ struct AttnArgs {
   AttnOut o;              // forward: o; backward: dq
   AttnOut dk, dv;         // backward
   float* lse;             // forward: [B, H, Tq] out
-  const float* stats;     // backward: [B H][2][Tq rounded up to 128]: lse in log2 units, then delta
+  const float* stats;     // backward: [B H][2][Tq rounded up to 128]: -lse in log2 units, then -delta
   float* records;         // partial records, two per CTA
-  unsigned int* counters; // arrivals per tile, all 0 between calls
+  float* dq_records;      // the dq kernel's
   unsigned int* err;
   unsigned long long timeout_ns;
 };
@@ -40,15 +40,32 @@ struct AttnPrepArgs {
   int B, H, Tq, d;
 };
 
-__host__ __device__ constexpr size_t attn_record_floats(int d) { return 2ull * 128 * d + 4 * 128; }   // the largest of the three kernels'
+__host__ __device__ constexpr size_t attn_record_floats(int d) { return 2ull * 128 * d + 4 * 128; }   // forward; dk and dv
+__host__ __device__ constexpr size_t attn_dq_record_floats(int d) { return 128ull * d; }
 cudaError_t attn_fwd_setup();
 cudaError_t attn_bwd_setup();
+// Each launches as a programmatic dependent of the one before it in the same call. combine: a
+// tile may be shared between CTAs, so its records have to be added up.
 cudaError_t launch_attn_fwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const AttnArgs& a, int ctas, cudaStream_t st);
-cudaError_t launch_attn_prep(bool half, const AttnPrepArgs& a, cudaStream_t st);
-cudaError_t launch_attn_dkv(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st);
-cudaError_t launch_attn_dq(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                           const CUtensorMap& g, const AttnArgs& a, int ctas, cudaStream_t st);
+                            const AttnArgs& a, int ctas, bool combine, cudaStream_t st);
+cudaError_t launch_attn_bwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const CUtensorMap& g, const AttnPrepArgs& prep, const AttnArgs& a, int ctas, bool combine,
+                            cudaStream_t st);
+// Launch a kernel, behind the preceding one in the stream if `dependent`.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool dependent,
+                           const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace arl2

@@ -1,9 +1,10 @@
-"""Fit the degree-3 polynomial behind exp2_poly() in arl2_device.cuh.
+"""Fit the polynomials behind exp2_poly() in arl2_device.cuh (degree 3) and exp2_poly4() in
+arl2_attn.cuh (degree 4).
 
     python softmax_attention_ar_b200/csrc/fit_exp2_poly.py
 
 Remez exchange for the polynomial p(f) ~ 2^f on [-1/2, 1/2] whose relative error
-(p(f) - 2^f) / 2^f equioscillates. It prints the float32 coefficients c0..c3 and the
+(p(f) - 2^f) / 2^f equioscillates. It prints the float32 coefficients c0, c1, .. and the
 maximum relative error of the float32 polynomial evaluated the way the kernel does
 (Horner with fused multiply-adds).
 """
@@ -48,14 +49,17 @@ def eval_f32(c, x):
     def fma(p, q, r):  # fp32 operands: the fp64 product is exact, one rounding of the sum to fp32
         return (p.astype(np.float64) * q + r).astype(np.float32)
 
-    p = fma(fma(fma(np.full_like(f, c[3]), f, c[2]), f, c[1]), f, c[0])
+    p = np.full_like(f, c[-1])
+    for ci in c[-2::-1]:
+        p = fma(p, f, ci)
     bits = p.view(np.int32) + (t.view(np.int32) << 23)
     return bits.view(np.float32)
 
 
 if __name__ == "__main__":
-    c = remez(3).astype(np.float32)
     xs = np.linspace(-125, 64, 2_000_001, dtype=np.float32)
-    rel = np.abs(eval_f32(c, xs).astype(np.float64) / np.exp2(xs.astype(np.float64)) - 1)
-    print("c0..c3 =", [float(v) for v in c])
-    print(f"max relative error over [-125, 64]: {rel.max():.3e}")
+    for deg in (3, 4):
+        c = remez(deg).astype(np.float32)
+        rel = np.abs(eval_f32(c, xs).astype(np.float64) / np.exp2(xs.astype(np.float64)) - 1)
+        print(f"degree {deg}: c0.. =", [float(v) for v in c])
+        print(f"max relative error over [-125, 64]: {rel.max():.3e}")

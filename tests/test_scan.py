@@ -8,8 +8,6 @@ each, so an input passes through fewer than 2 T + 80 roundings; the error of h_t
 over absolute values, and a stored value is off by half a step of its type on top
 (eps / 2 relative, and half the smallest subnormal of fp16).
 """
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -332,15 +330,15 @@ def test_c_entry_refuses_without_a_gpu():
     lib = arl2.load_library()
     p = 1 << 20   # an aligned address; never dereferenced by the argument checks
 
-    def fwd(B=2, T=8, C=64, heads=0, dtype=2, gate=2, x=p, a=p, h=p, h0=None, xs=(512, 64), as_=(512, 64, 0),
-            hs=(512, 64), ws=None):
-        f = arl2._ScanFwd(arl2._ScanShape(B, T, C, heads, dtype, gate, None), x, a, h0, h, None, ws, xs, as_, hs)
-        return lib.arl2_scan_forward(ctypes.byref(f), None)
+    def fwd(B=2, T=8, C=64, heads=0, dtype=2, gate=2, x=p, a=p, h=p, h0=0, xs=(512, 64), as_=(512, 64, 0),
+            hs=(512, 64), ws=0):
+        f = arl2._SCAN_FWD.pack(B, T, C, heads, dtype, gate, 0, x, a, h0, h, 0, ws, *xs, *as_, *hs)
+        return lib.arl2_scan_forward(f, None)
 
     bad, unsup = arl2.ARL2_ERR_INVALID_ARG, arl2.ARL2_ERR_UNSUPPORTED
     assert lib.arl2_scan_forward(None, None) == bad and lib.arl2_scan_backward(None, None) == bad
     assert fwd(B=0) == bad and fwd(T=0) == bad and fwd(C=0) == bad and fwd(heads=-1) == bad
-    assert fwd(x=None) == bad and fwd(a=None) == bad and fwd(h=None) == bad
+    assert fwd(x=0) == bad and fwd(a=0) == bad and fwd(h=0) == bad
     assert fwd(x=p + 2) == bad and fwd(h0=p + 2) == bad
     assert fwd(dtype=3) == bad and fwd(gate=7) == bad
     assert fwd(gate=0) == unsup                       # fp32 values with bf16 gates
@@ -351,13 +349,13 @@ def test_c_entry_refuses_without_a_gpu():
     assert fwd(hs=(0, 64)) == bad and fwd(hs=(512, 32)) == bad and fwd(hs=(256, 64)) == bad
     assert lib.arl2_scan_workspace_bytes(None) == 0
     assert fwd(B=1, T=5000, xs=(0, 64), as_=(0, 64, 0), hs=(0, 64)) == bad   # needs a workspace
-    sh = arl2._ScanShape(2, 8, 64, 0, 2, 2, None)
+    sh = (2, 8, 64, 0, 2, 2, 0)
     s2, s3 = (512, 64), (512, 64, 0)
     for hole in range(5):
         q = [p] * 5
-        q[hole] = None
+        q[hole] = 0
         dh, a, h, dx, da = q
-        f = arl2._ScanBwd(sh, dh, a, h, None, None, dx, da, None, None, s2, s3, s2, s2)
-        assert lib.arl2_scan_backward(ctypes.byref(f), None) == bad
-    f = arl2._ScanBwd(sh, p, p, p, None, None, p, p, None, None, s2, s3, s2, (512, 0))
-    assert lib.arl2_scan_backward(ctypes.byref(f), None) == bad
+        f = arl2._SCAN_BWD.pack(*sh, dh, a, h, 0, 0, dx, da, 0, 0, *s2, *s3, *s2, *s2)
+        assert lib.arl2_scan_backward(f, None) == bad
+    f = arl2._SCAN_BWD.pack(*sh, p, p, p, 0, 0, p, p, 0, 0, *s2, *s3, *s2, 512, 0)
+    assert lib.arl2_scan_backward(f, None) == bad
