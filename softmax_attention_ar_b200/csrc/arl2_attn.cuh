@@ -342,6 +342,16 @@ __device__ __forceinline__ void mma_over_rows(uint32_t d_tmem, uint32_t a, uint3
   mma8_ts(d_tmem, a, col, desc_mnmajor(b_tile, 0), idesc, acc);
 }
 
+// Steps [4 kHalf, 4 kHalf + 4) of it, with kSplit = 0.
+template <int kHalf>
+__device__ __forceinline__ void mma_over_half_rows(uint32_t d_tmem, uint32_t a, uint32_t b_tile, uint32_t idesc,
+                                                   uint32_t acc) {
+  const uint64_t b0 = desc_mnmajor(b_tile, 0);
+#pragma unroll
+  for (int s = 4 * kHalf; s < 4 * kHalf + 4; ++s)
+    mma_bf16_ts(d_tmem, a + 8 * s, b0 + mnmajor_step16(s), idesc, s > 0 ? 1u : acc);
+}
+
 // Registers per thread of the calling warpgroup (all four of its warps): give some back, or take
 // them. The sum over the block must not exceed what it was launched with.
 template <int kRegs>

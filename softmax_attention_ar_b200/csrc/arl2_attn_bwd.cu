@@ -307,43 +307,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int u = sg.kb; u < sg.ke; ++u, ++n) {
         const bool more = u + 1 < sg.ke;
         const uint32_t acc = u > sg.kb;
-        ok = mbar_wait_warp(bar(kKPReady), n & 1, g);
-        if (ok && !acc && ns > 0) ok = mbar_wait_warp(bar(kKAccEmpty), (ns - 1) & 1, g);
+        // Everything but P first: what is left after P's arrival is on the critical path.
+        if (!acc && ns > 0) ok = mbar_wait_warp(bar(kKAccEmpty), (ns - 1) & 1, g);
+        ok = ok && (!more || q_full(n + 1)) && mbar_wait_warp(bar(kKPReady), n & 1, g);
         if (!ok) break;
         tc_fence_after();
         if (lead) {
           mma_over_rows<32>(c_dv, c_s, g_at(n), id_d, acc);
-          mma_commit(bar(kKGEmpty + n % 2));
-        }
-        __syncwarp();
-        if (more) {
-          ok = q_full(n + 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lead) {
+          if (more) {
             mma_over_d<D>(c_s, k_tile, q_at(n + 1), id_s);
             mma_commit(bar(kKSFull));
           }
-          __syncwarp();
+          mma_commit(bar(kKGEmpty + n % 2));
         }
-        ok = mbar_wait_warp(bar(kKDReady), n & 1, g);
+        __syncwarp();
+        ok = (!more || g_full(n + 1)) && mbar_wait_warp(bar(kKDReady), n & 1, g);
         if (!ok) break;
         tc_fence_after();
         if (lead) {
           mma_over_rows<32>(c_dk, c_dp, q_at(n), id_d, acc);
-          mma_commit(bar(kKQEmpty + n % 3));
-        }
-        __syncwarp();
-        if (more) {
-          ok = g_full(n + 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lead) {
+          if (more) {
             mma_over_d<D>(c_dp, v_tile, g_at(n + 1), id_s);
             mma_commit(bar(kKDFull));
           }
-          __syncwarp();
+          mma_commit(bar(kKQEmpty + n % 3));
         }
+        __syncwarp();
       }
       if (!ok) break;
       if (lead) {
@@ -385,10 +374,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int row0 = first_row(a.mask, j);   // the first query row that sees this key
       int i = first + sg.kb % per_head;
       for (int u = sg.kb; u < sg.ke; ++u, ++n) {
-        ok = mbar_wait_warp(bar(kKTFull + n % 2), (n / 2) & 1, g) && mbar_wait_warp(bar(kKSFull), n & 1, g);
+        ok = mbar_wait_warp(bar(kKTFull + n % 2), (n / 2) & 1, g);
+        if (!ok) break;
+        // The statistics come to registers while the scores are not there yet: shared memory is busy
+        // with the MMAs' operands, and a load behind them is slow.
+        const float4* st = reinterpret_cast<const float4*>(attn_smem + 7 * TO::kBytes + n % 2 * 1024) + 16 * wg;
+        float4 lse[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) lse[k] = st[k];
+        ok = mbar_wait_warp(bar(kKSFull), n & 1, g);
         if (!ok) break;
         tc_fence_after();
-        const float4* st = reinterpret_cast<const float4*>(attn_smem + 7 * TO::kBytes + n % 2 * 1024) + 16 * wg;
         const int hidden = row0 - (i * kRows + 64 * wg);   // this thread's columns below it see nothing
         float2 p[32];
         {
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
 #pragma unroll
           for (int k = 0; k < 64; k += 4) {
-            const float4 l = st[k / 4];
+            const float4 l = lse[k / 4];
             const uint32_t* x = &s[k >> 5][k & 31];
             const float2 x0 = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
             const float2 x1 = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
@@ -606,17 +602,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ok = mbar_wait_warp(bar(kQQFull), ns & 1, g) && scores(n) && grads(n) && (cnt < 2 || scores(n + 1));
       if (!ok) break;
       for (int u = 0; u < cnt; ++u, ++n) {
-        ok = mbar_wait_warp(bar(kQDReady), n & 1, g);
-        if (ok && u + 1 < cnt) ok = grads(n + 1);   // first: the next softmax waits for it
-        if (ok && u == 0 && ns > 0) ok = mbar_wait_warp(bar(kQAccEmpty), (ns - 1) & 1, g);
+        // Everything but dS first: what is left after its arrival is on the critical path.
+        const bool more = u + 1 < cnt, more2 = u + 2 < cnt;
+        if (u == 0 && ns > 0) ok = mbar_wait_warp(bar(kQAccEmpty), (ns - 1) & 1, g);
+        ok = ok && (!more || v_full(n + 1)) && mbar_wait_warp(bar(kQDReady), n & 1, g);
         if (!ok) break;
         tc_fence_after();
         if (lead) {
+          if (more) {   // first: the next softmax waits for it
+            mma_over_d<D>(c_dp, g_tile, v_ring + (n + 1) % 2 * TO::kBytes, id_s);
+            mma_commit(bar(kQDFull));
+            mma_commit(bar(kQVEmpty + (n + 1) % 2));
+          }
           mma_over_rows<32>(c_dq, tmem + 128u * (n & 1), k_at(n), id_d, u > 0);
           mma_commit(bar(kQKEmpty + n % 3));
         }
         __syncwarp();
-        if (u + 2 < cnt) ok = scores(n + 2);
+        ok = !more2 || scores(n + 2);
         if (!ok) break;
       }
       if (!ok) break;

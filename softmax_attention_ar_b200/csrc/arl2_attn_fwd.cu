@@ -16,7 +16,8 @@
 // thread = row = TMEM lane. TMEM: S0, S1 (columns 0, 128; the packed P overwrites the first 64
 // of its S), O0, O1 (256, 384). One issuing thread keeps the MMAs that touch the same columns
 // in order; the rest is ordered by barriers:
-//   - S full (commit) -> softmax; P ready (4 warps) -> P V MMA; the commit of S(t + 1) also says
+//   - S full (commit) -> softmax; P ready (4 warps, by halves of the keys, so that the first half's
+//     product runs while the second is made) -> P V MMA; the commit of S(t + 1) also says
 //     that P V (t) is done, so the softmax may rescale O before it hands over P (t + 1);
 //   - O full -> epilogue, O empty -> the next segment's first P V.
 #include <algorithm>
@@ -36,8 +37,8 @@ enum : int {
   kFFull = 2,              // + stage
   kFEmpty = kFFull + kRing,
   kFSFull = kFEmpty + kRing,   // + query tile (2)
-  kFPReady = kFSFull + 2,
-  kFOFull = kFPReady + 2,
+  kFPReady = kFSFull + 2,      // + 2 query tile + half (4)
+  kFOFull = kFPReady + 4,
   kFOEmpty = kFOFull + 2,
   kFSide = kFOEmpty + 2,
   kFFinal = kFSide + 1,
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   griddep_launch_dependents();   // the combining launch waits for this grid's end before it reads
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFBars; ++i) {
-      const bool by4 = (i >= kFPReady && i < kFPReady + 2) || (i >= kFOEmpty && i < kFOEmpty + 2);
+      const bool by4 = (i >= kFPReady && i < kFPReady + 4) || (i >= kFOEmpty && i < kFOEmpty + 2);
       mbar_init(bar(i), i == kFFinal ? 9 : by4 ? 4 : 1);
     }
     *abort_flag = 0;
@@ -185,29 +186,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       __syncwarp();
       for (int t = 0; ok && t < n; ++t, r += 2) {
         const bool more = t + 1 < n;
-        for (int i = 0; i < tiles; ++i) {
-          ok = mbar_wait_warp(bar(kFPReady + i), np[i] & 1, g);
-          if (ok && t == 0 && nseg[i] > 0) ok = mbar_wait_warp(bar(kFOEmpty + i), (nseg[i] - 1) & 1, g);
-          if (ok && i == 0) ok = full(r + 1);
+        // Everything but P first: what is left after P's arrival is on the critical path.
+        ok = full(r + 1) && (!more || full(r + 2));
+        for (int i = 0; ok && i < tiles; ++i) {
+          if (t == 0 && nseg[i] > 0) ok = mbar_wait_warp(bar(kFOEmpty + i), (nseg[i] - 1) & 1, g);
+          ok = ok && mbar_wait_warp(bar(kFPReady + 2 * i), np[i] & 1, g);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead)
+            mma_over_half_rows<0>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, t > 0);
+          __syncwarp();
+          ok = mbar_wait_warp(bar(kFPReady + 2 * i + 1), np[i] & 1, g);
           if (!ok) break;
           ++np[i];
           tc_fence_after();
           if (lead) {
-            mma_over_rows<0>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, t > 0);
-            if (i + 1 == tiles) mma_commit(bar(kFEmpty + (r + 1) % kRing));
-          }
-          __syncwarp();
-          if (more) {
-            if (i == 0) ok = full(r + 2);
-            if (!ok) break;
-            tc_fence_after();
-            if (lead) {
+            mma_over_half_rows<1>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, 1u);
+            if (more) {
               mma_over_d<D>(tmem + 128u * i, q_tile + i * TO::kBytes, slot(r + 2), id_s);
               mma_commit(bar(kFSFull + i));
-              if (i + 1 == tiles) mma_commit(bar(kFEmpty + (r + 2) % kRing));
+            } else {
+              mma_commit(bar(kFOFull + i));
             }
-          } else if (lead) {
-            mma_commit(bar(kFOFull + i));
+            if (i + 1 == tiles) {
+              mma_commit(bar(kFEmpty + (r + 1) % kRing));
+              if (more) mma_commit(bar(kFEmpty + (r + 2) % kRing));
+            }
           }
           __syncwarp();
         }
@@ -322,13 +326,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             p[k] = pack2<kHalf>(e[k].x, e[k].y);
           }
           tmem_st16(s_col + 16 * q, p);
+          if (q & 1) {   // half of the keys: their product may start
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(bar(kFPReady + 2 * i + (q >> 1)));
+          }
         }
         sum[0] = __fadd2_rn(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
         if (!(tile_top < INFINITY)) l = NAN;   // a NaN or +inf among the scores: the row has no softmax
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(bar(kFPReady + i));
       }
       if (ok) ok = mbar_wait_warp(bar(kFOFull + i), nseg & 1, g);
       if (!ok) break;
