@@ -515,6 +515,8 @@ def _scan_shape(x, a, lens, name):
 
 
 def _scan_workspace(lib, fields, x):
+    if fields[1] <= 512:   # one chunk, whatever the width
+        return None
     n = lib.arl2_scan_workspace_bytes(struct.pack(_SCAN_SHAPE, *fields))
     return x.new_empty(n, dtype=torch.uint8) if n else None
 
@@ -541,11 +543,11 @@ def _scan_forward(x, a, h0, out, final, stream, index, shape, st_a, fields):
     lib = load_library()
     _want(h0, "h0", index, _F32, (B, C), True)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _want(out, "out", index, (x.dtype,), shape)
     if final is None:
-        final = x.new_empty((B, C), dtype=torch.float32)
+        final = x.new_empty((B, C), dtype=torch.float32) if h0 is None else torch.empty_like(h0)
     else:
         _want(final, "final", index, _F32, (B, C), True)
     ws = _scan_workspace(lib, fields, x)
@@ -580,11 +582,11 @@ def _scan_backward(dh, a, h, h0, dfinal, dx, da, dh0, stream, index, shape, st_a
     _want(h0, "h0", index, _F32, (B, C), True)
     _want(dfinal, "dfinal", index, _F32, (B, C), True)
     if dx is None:
-        dx = dh.new_empty(shape)
+        dx = torch.empty_like(dh, memory_format=torch.contiguous_format)
     else:
         _want(dx, "dx", index, (dh.dtype,), shape)
     if da is None:
-        da = a.new_empty(a.shape)
+        da = torch.empty_like(a, memory_format=torch.contiguous_format)
     else:
         _want(da, "da", index, (a.dtype,), a.shape, True)
     if dh0 is None:
@@ -699,7 +701,7 @@ class SoftmaxAttention:
         qs, ks = (self.B, shape[0], self.H, self.d), (self.B, shape[1], self.H_kv, self.d)
         fields = self._tensor(q, "q", qs) + self._tensor(k, "k", ks) + self._tensor(v, "v", ks)
         if out is None:
-            out = q.new_empty(qs)
+            out = torch.empty_like(q)
         if lse is None:
             lse = q.new_empty((self.B, self.H, shape[0]), dtype=torch.float32)
         else:
@@ -727,9 +729,9 @@ class SoftmaxAttention:
         if lse is None:
             raise TypeError("lse must be a torch.Tensor")
         _want(lse, "lse", self._index, _F32, (self.B, self.H, shape[0]), True)
-        dq = q.new_empty(qs) if dq is None else dq
-        dk = q.new_empty(ks) if dk is None else dk
-        dv = q.new_empty(ks) if dv is None else dv
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
         f = _ATTN_BWD.pack(*shape, *fields, *self._tensor(dq, "dq", qs), *self._tensor(dk, "dk", ks),
                            *self._tensor(dv, "dv", ks), lse.data_ptr())
         _check(self._lib.arl2_attn_backward(self._c, f, stream), "arl2_attn_backward")

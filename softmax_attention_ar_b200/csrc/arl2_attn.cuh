@@ -73,6 +73,11 @@ struct KeyTiles {
   }
 };
 
+// x / y for x, y > 0 (x >= 0): a 64-bit division takes several times as long.
+__device__ __forceinline__ long long quick_div(long long x, long long y) {
+  return (x | y) >> 32 == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
+
 // Where a CTA's range starts; computed by one warp, read by every role.
 struct Split {
   long long u0, u1, total;
@@ -122,12 +127,12 @@ __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c
   s.ctas = static_cast<int>(ctas);
   s.total = total;
   if (c < ctas) {
-    s.u0 = c * total / ctas;
-    s.u1 = (c + 1) * total / ctas;
+    s.u0 = quick_div(c * total, ctas);
+    s.u1 = quick_div((c + 1) * total, ctas);
     long long r = s.u0;
     if (!ragged) {
       const long long per_batch = per_head * heads;
-      s.b = static_cast<int>(r / per_batch);
+      s.b = static_cast<int>(quick_div(r, per_batch));
       r -= s.b * per_batch;
     } else {
       for (; s.b < B; ++s.b) {
@@ -136,13 +141,13 @@ __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c
         r -= per_head * heads;
       }
     }
-    s.h = static_cast<int>(r / per_head);
+    s.h = static_cast<int>(quick_div(r, per_head));
     r -= s.h * per_head;
     const int ql = q_length(m, s.b), kl = k_length(m, s.b), n = Tiles::count(m);
     if (m.F == 0) {
       const int v = Tiles::valid(m, ql, kl), w = max(1, Tiles::units(m, 0, ql, kl, group));
       if (r < static_cast<long long>(v) * w) {
-        s.tile = static_cast<int>(r / w);
+        s.tile = static_cast<int>(quick_div(r, w));
         s.off = static_cast<int>(r - static_cast<long long>(s.tile) * w);
       } else {
         s.tile = v + static_cast<int>(r - static_cast<long long>(v) * w);
@@ -217,10 +222,10 @@ struct Walk {
 // is `first`: a CTA has at most two segments of tiles it shares, the first and the last of its
 // range.
 __device__ __forceinline__ int unit_owner(const Split& s, long long u) {
-  return static_cast<int>(((u + 1) * s.ctas - 1) / s.total);
+  return static_cast<int>(quick_div((u + 1) * s.ctas - 1, s.total));
 }
 __device__ __forceinline__ int record_slot(const Split& s, int c, long long first) {
-  return 2 * c + (c * s.total / s.ctas >= first ? 0 : 1);
+  return 2 * c + (quick_div(c * s.total, s.ctas) >= first ? 0 : 1);
 }
 
 // ------------------------------------------------------------------ element types

@@ -255,12 +255,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         continue;
       }
       const int limit = in_q ? key_limit(a.mask, row, sg.kl) : 0;
+      // A warp without a row inside the length leaves its P and O as they are: an MMA's rows do not
+      // mix, and these are not written. (One query: 67 us instead of 104 over four long caches.)
+      const bool idle = row - (r & 31) >= sg.ql;
       float m = -INFINITY, l = 0.f;
       for (int t = sg.kb; t < sg.ke; ++t) {
         ok = mbar_wait_warp(bar(kFSFull + i), nt & 1, g);
         if (!ok) break;
         ++nt;
         tc_fence_after();
+        if (idle) {
+          warp_arrive(bar(kFPReady + 2 * i));
+          warp_arrive(bar(kFPReady + 2 * i + 1));
+          continue;
+        }
         uint32_t s[4][32];
         tmem_ld32x2_wait(s_col, s[0], s_col + 32, s[1]);
         tmem_ld32x2_wait(s_col + 64, s[2], s_col + 96, s[3]);
@@ -407,10 +415,7 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const _
   const int units = max(1, FwdTiles::units(a.mask, sp.tile, ql, kl, 1));
   const int c1 = unit_owner(sp, first + units - 1);
   const bool sees = row < ql && key_limit(a.mask, row, kl) > 0;
-  float m = -INFINITY;
-  for (int j = c - 1; j <= c1; ++j)
-    m = fmaxf(m, __ldcg(fwd_record<D>(a, record_slot(sp, j, first)) + 2 * kRows * D + i * 2 * kRows + r));
-  float l = 0.f, y[32] = {};
+  float m = -INFINITY, l = 0.f, y[32] = {};
 #pragma unroll 2
   for (int j = c - 1; j <= c1; ++j) {
     const float* rec = fwd_record<D>(a, record_slot(sp, j, first));
@@ -419,14 +424,16 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const _
     float4 x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __ldcg(o + e * kRows);
-    const float mj = __ldcg(ml), w = mj == -INFINITY ? 0.f : exp2f(mj - m);
-    l = fmaf(__ldcg(ml + kRows), w, l);
+    const float mj = __ldcg(ml), lj = __ldcg(ml + kRows), top = fmaxf(m, mj);
+    const float keep = m == -INFINITY ? 0.f : exp2f(m - top), w = mj == -INFINITY ? 0.f : exp2f(mj - top);
+    m = top;
+    l = l * keep + (lj != lj ? lj : lj * w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[4 * e] = fmaf(x[e].x, w, y[4 * e]);
-      y[4 * e + 1] = fmaf(x[e].y, w, y[4 * e + 1]);
-      y[4 * e + 2] = fmaf(x[e].z, w, y[4 * e + 2]);
-      y[4 * e + 3] = fmaf(x[e].w, w, y[4 * e + 3]);
+      y[4 * e] = fmaf(x[e].x, w, y[4 * e] * keep);
+      y[4 * e + 1] = fmaf(x[e].y, w, y[4 * e + 1] * keep);
+      y[4 * e + 2] = fmaf(x[e].z, w, y[4 * e + 2] * keep);
+      y[4 * e + 3] = fmaf(x[e].w, w, y[4 * e + 3] * keep);
     }
   }
   if (row >= a.mask.Tq) return;

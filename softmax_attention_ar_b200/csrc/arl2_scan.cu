@@ -589,6 +589,18 @@ arl2_status check(const arl2_scan_shape& s, bool* head) {
   return ARL2_OK;
 }
 
+// The current device, checked on its first call.
+arl2_status current_device(int* dev) {
+  static std::atomic<unsigned long long> known{0};
+  if (cudaGetDevice(dev) != cudaSuccess) return ARL2_ERR_CUDA;
+  if (*dev < 0 || *dev > 63) return ARL2_ERR_UNSUPPORTED;
+  if (known.load(std::memory_order_acquire) >> *dev & 1) return ARL2_OK;
+  int sms = 0;
+  const arl2_status s = static_cast<arl2_status>(prepare_device(dev, &sms));
+  if (s == ARL2_OK) known.fetch_or(1ull << *dev, std::memory_order_release);
+  return s;
+}
+
 size_t workspace_bytes(const arl2_scan_shape& s) {
   // Whether groups of 4 channels can be accessed at once is known only with the pointers.
   size_t pairs = 0;
@@ -628,10 +640,9 @@ extern "C" arl2_status arl2_scan_forward(const arl2_scan_fwd* f, arl2_stream str
   if (head && !wide) return ARL2_ERR_INVALID_ARG;
   if (!head) wide = wide && wide_ok(f->a, ge, as);
   if (needs_workspace(s) && !(f->workspace && at(f->workspace, 16))) return ARL2_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  const arl2_status ds = static_cast<arl2_status>(prepare_device(&dev, &sms));
+  int dev = 0;
+  const arl2_status ds = current_device(&dev);
   if (ds != ARL2_OK) return ds;
-  if (dev < 0 || dev > 63) return ARL2_ERR_UNSUPPORTED;
   ScanParams p{};
   p.in = f->x;
   p.a = f->a;
@@ -669,10 +680,9 @@ extern "C" arl2_status arl2_scan_backward(const arl2_scan_bwd* f, arl2_stream st
   if (head && !wide) return ARL2_ERR_INVALID_ARG;
   if (!head) wide = wide && wide_ok(f->a, ge, as) && at(f->da, 4 * ge);
   if (needs_workspace(s) && !(f->workspace && at(f->workspace, 16))) return ARL2_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  const arl2_status ds = static_cast<arl2_status>(prepare_device(&dev, &sms));
+  int dev = 0;
+  const arl2_status ds = current_device(&dev);
   if (ds != ARL2_OK) return ds;
-  if (dev < 0 || dev > 63) return ARL2_ERR_UNSUPPORTED;
   ScanParams p{};
   p.in = f->dh;
   p.a = f->a;
