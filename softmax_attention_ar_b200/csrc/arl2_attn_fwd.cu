@@ -11,6 +11,10 @@
 // rarely; m, the sum l and the accumulator are fp32, only the probabilities (below 2^8) are
 // rounded to 16 bits for the second product.
 //
+// A narrow tile, with rows in its first query tile only (few queries, a ragged end), would leave
+// half of the softmax idle and the copies waiting for a chain of score, softmax and product: there
+// the two groups take the key tiles by turns, and the first adds both accumulators up at the end.
+//
 // Roles (384 threads, one CTA per SM): warp 0 copies (Q per segment; K and V tiles through a
 // ring of 5), warp 1 issues every MMA, warps 4-7 and 8-11 are the softmax of query tile 0 and 1,
 // thread = row = TMEM lane. TMEM: S0, S1 (columns 0, 128; the packed P overwrites the first 64
@@ -41,10 +45,12 @@ enum : int {
   kFOFull = kFPReady + 4,
   kFOEmpty = kFOFull + 2,
   kFSide = kFOEmpty + 2,
-  kFFinal = kFSide + 1,
+  kFPairFull = kFSide + 1,   // narrow tiles: group 1's m and l are there (4 warps)
+  kFPairEmpty,               // and were read (4 warps)
+  kFFinal,
   kFBars = kFFinal + 1
 };
-constexpr uint32_t kFCtl = 512;   // barriers, split, flags
+constexpr uint32_t kFCtl = 512 + 1024;   // barriers, split, flags; m and l of narrow tiles [2][128]
 static_assert(kFBars * 8 <= 256 && sizeof(Split) + 32 <= 256, "control block");
 template <int D>
 constexpr uint32_t fwd_smem() {
@@ -90,7 +96,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   griddep_launch_dependents();   // the combining launch waits for this grid's end before it reads
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFBars; ++i) {
-      const bool by4 = (i >= kFPReady && i < kFPReady + 4) || (i >= kFOEmpty && i < kFOEmpty + 2);
+      const bool by4 = (i >= kFPReady && i < kFPReady + 4) || (i >= kFOEmpty && i < kFOEmpty + 2) ||
+                       i == kFPairFull || i == kFPairEmpty;
       mbar_init(bar(i), i == kFFinal ? 9 : by4 ? 4 : 1);
     }
     *abort_flag = 0;
@@ -176,6 +183,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       ok = mbar_wait_warp(bar(kFQFull), ns & 1, g) && full(r);
       if (!ok) break;
       tc_fence_after();
+      if (tiles == 1) {
+        // Narrow: the two groups take the key tiles by turns, each with an S and an O of its own.
+        for (int t = 0; ok && t < min(n, 2); ++t) {
+          ok = full(r + 2 * t);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+            mma_over_d<D>(tmem + 128u * t, q_tile, slot(r + 2 * t), id_s);
+            mma_commit(bar(kFSFull + t));
+            mma_commit(bar(kFEmpty + (r + 2 * t) % kRing));
+          }
+          __syncwarp();
+        }
+        for (int t = 0; ok && t < n; ++t, r += 2) {
+          const int i = t & 1;
+          ok = full(r + 1) && (t + 2 >= n || full(r + 4));
+          if (ok && t < 2 && nseg[i] > 0) ok = mbar_wait_warp(bar(kFOEmpty + i), (nseg[i] - 1) & 1, g);
+          ok = ok && mbar_wait_warp(bar(kFPReady + 2 * i), np[i] & 1, g);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) mma_over_half_rows<0>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, t > 1);
+          __syncwarp();
+          ok = mbar_wait_warp(bar(kFPReady + 2 * i + 1), np[i] & 1, g);
+          if (!ok) break;
+          ++np[i];
+          tc_fence_after();
+          if (lead) {
+            mma_over_half_rows<1>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, 1u);
+            mma_commit(bar(kFEmpty + (r + 1) % kRing));
+            if (t + 2 < n) {
+              mma_over_d<D>(tmem + 128u * i, q_tile, slot(r + 4), id_s);
+              mma_commit(bar(kFSFull + i));
+              mma_commit(bar(kFEmpty + (r + 4) % kRing));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lead) {
+          mma_commit(bar(kFOFull));
+          mma_commit(bar(kFQEmpty));
+        }
+        __syncwarp();
+        ++ns;
+        ++nseg[0];
+        ++nseg[1];
+        continue;
+      }
       if (lead) {
         for (int i = 0; i < tiles; ++i) {
           mma_over_d<D>(tmem + 128u * i, q_tile + i * TO::kBytes, slot(r), id_s);
@@ -237,13 +292,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
     const uint32_t s_col = tmem + lanes + 128u * i, o_col = tmem + lanes + 256u + 128u * i;
     const float to_log2 = a.scale * 1.4426950408889634f;
-    uint32_t nt = 0, nseg = 0;
+    uint32_t nt = 0, nseg = 0, npair = 0;
+    float* pair = reinterpret_cast<float*>(gctl + 512);
     const int c = static_cast<int>(blockIdx.x);
     bool ok = true;
     while (ok && walk.next(sg)) {
-      const int row = sg.tile * kFwdRows + i * kRows + r;
-      const bool in_q = row < sg.ql;
+      const bool narrow = sg.units > 0 && sg.tile * kFwdRows + kRows >= sg.ql;   // one query tile
       float* lse = a.lse + (static_cast<size_t>(sg.b) * a.H + sg.h) * a.mask.Tq;
+      int row = sg.tile * kFwdRows + i * kRows + r;
       if (sg.units == 0 || sg.tile * kFwdRows + i * kRows >= sg.ql) {
         // Nothing to see, or rows behind the length: zeros, once per tile.
         if (sg.kb == 0 && row < a.mask.Tq) {
@@ -252,14 +308,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int k = 0; k < D; k += 32) store_row<D, kHalf>(a, sg.b, sg.h, row, z, k);
           lse[row] = -INFINITY;
         }
-        continue;
+        if (!narrow) continue;
+        row -= i * kRows;   // group 1 helps with the first query tile
       }
+      const bool in_q = row < sg.ql;
       const int limit = in_q ? key_limit(a.mask, row, sg.kl) : 0;
       // A warp without a row inside the length leaves its P and O as they are: an MMA's rows do not
-      // mix, and these are not written. (One query: 67 us instead of 104 over four long caches.)
+      // mix, and these are not written.
       const bool idle = row - (r & 31) >= sg.ql;
       float m = -INFINITY, l = 0.f;
-      for (int t = sg.kb; t < sg.ke; ++t) {
+      const int step = narrow ? 2 : 1, t0 = sg.kb + (narrow ? i : 0);
+      for (int t = t0; t < sg.ke; t += step) {
         ok = mbar_wait_warp(bar(kFSFull + i), nt & 1, g);
         if (!ok) break;
         ++nt;
@@ -298,7 +357,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float f = raise && m != -INFINITY ? ex2_approx(m - m_new) : 1.f;
           l *= f;
           m = m_new;
-          if (t > sg.kb) {
+          if (t > t0) {
 #pragma unroll 1
             for (int k = 0; k < D; k += 32) {
               uint32_t x[32];
@@ -344,23 +403,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         l += sum[0].x + sum[0].y;
         if (!(tile_top < INFINITY)) l = NAN;   // a NaN or +inf among the scores: the row has no softmax
       }
-      if (ok) ok = mbar_wait_warp(bar(kFOFull + i), nseg & 1, g);
+      if (!ok) break;
+      if (narrow && i == 1) {   // m and l to group 0, which finishes the rows
+        if (npair > 0) ok = mbar_wait_warp(bar(kFPairEmpty), (npair - 1) & 1, g);
+        if (!ok) break;
+        ++npair;
+        pair[r] = m;
+        pair[kRows + r] = l;
+        warp_arrive(bar(kFPairFull));
+        continue;
+      }
+      ok = mbar_wait_warp(bar(kFOFull + i), nseg & 1, g);
       if (!ok) break;
       ++nseg;
+      // Narrow: O = keep O0 + add O1.
+      float keep = 1.f, add = 0.f;
+      if (narrow) {
+        ok = mbar_wait_warp(bar(kFPairFull), npair & 1, g);
+        if (!ok) break;
+        ++npair;
+        const float m1 = pair[r], l1 = pair[kRows + r], top = fmaxf(m, m1);
+        warp_arrive(bar(kFPairEmpty));
+        keep = m == -INFINITY ? 0.f : exp2f(m - top);
+        add = m1 == -INFINITY ? 0.f : exp2f(m1 - top);
+        l = l * keep + (l1 != l1 ? l1 : l1 * add);
+        m = top;
+      }
+      const bool two = narrow && sg.ke - sg.kb > 1;
       tc_fence_after();
+      auto load_o = [&](int k, uint32_t (&x)[32]) {
+        if (!two) {
+          tmem_ld32_wait(o_col + k, x);
+        } else {
+          uint32_t z[32];
+          tmem_ld32x2_wait(o_col + k, x, o_col + 128 + k, z);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[e] = __float_as_uint(__uint_as_float(x[e]) * keep + (add == 0.f ? 0.f : __uint_as_float(z[e]) * add));
+        }
+      };
+      auto release_o = [&] {
+        tc_fence_before();
+        warp_arrive(bar(kFOEmpty + i));
+        if (narrow) warp_arrive(bar(kFOEmpty + 1));
+      };
       if (sg.whole) {
         const float f = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           uint32_t x[32];
           float y[32];
-          tmem_ld32_wait(o_col + k, x);
+          load_o(k, x);
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = in_q && limit > 0 ? __uint_as_float(x[e]) * f : 0.f;
           if (row < a.mask.Tq) store_row<D, kHalf>(a, sg.b, sg.h, row, y, k);
         }
-        tc_fence_before();
-        warp_arrive(bar(kFOEmpty + i));
+        release_o();
         if (row < a.mask.Tq) lse[row] = in_q && limit > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         continue;
       }
@@ -371,14 +469,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         uint32_t x[32];
-        tmem_ld32_wait(o_col + k, x);
+        load_o(k, x);
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
           ro[(k + e) / 4 * kRows + r] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
                                                    __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
       }
-      tc_fence_before();
-      warp_arrive(bar(kFOEmpty + i));
+      release_o();
       rml[r] = m;
       rml[kRows + r] = l;
     }
