@@ -6,18 +6,21 @@
 // sum over the head's channels). Both directions are the same scan: (A, X) pairs compose as
 // (A2, X2) after (A1, X1) = (A1 A2, A2 X1 + X2).
 //
-// The work is a few operations per element read, so memory traffic bounds it. A warp owns a
-// slice of consecutive tokens of 32 V channels and streams it; the kWarps slices of a CTA
-// follow one another and form a chunk. Two launches:
+// The work is a few operations per element read, so memory traffic bounds it, provided that few
+// instructions are spent per byte: a lane takes V channels, 16 bytes, at once. `lanes` lanes hold
+// a row of a channel group; they own a slice of consecutive tokens and stream it through a ring
+// in shared memory (cp.async, each lane copying what it reads itself, so no barrier is needed).
+// The slices of a CTA follow one another in time and form a chunk. Two launches:
 //   - arl2_scan_pairs_kernel reads x (dh) and a, and writes the (A, X) of every slice and of
 //     every chunk to the workspace;
 //   - arl2_scan_apply_kernel composes the pairs before each slice onto the initial state,
 //     then streams the slice again from that state and writes the results.
-// The second reading is what this costs over a single pass; it comes from L2 where x and a
-// fit there. A single-pass form (the cluster's CTAs following one another in time, pairs
+// The second reading is what this costs over a single pass. It comes from L2 as far as x and a fit
+// there: the first launch goes through each slice from its end to its start, so that the second
+// begins with what was read last, and results are stored evict-first. A single-pass form (a cluster's CTAs following one another in time, pairs
 // exchanged through distributed shared memory, data kept in a ring) reads everything once but
 // moves in lock step with a barrier per 1024 tokens: it measured 115 us on 32760 tokens of
-// 1536 bf16 channels, this form 73 us. A sequence that one chunk holds takes one launch, without workspace.
+// 1536 bf16 channels. A sequence that one chunk holds takes one launch, without workspace.
 // The order of all products and sums is fixed, so results do not depend on timing. All of it is
 // fp32; only the stored h, dx and da are rounded, once, to their types.
 #include <algorithm>
@@ -34,9 +37,9 @@
 namespace arl2 {
 namespace {
 
-constexpr int kWarps = 8;    // slices per chunk, warps per CTA
-constexpr int kBatch = 4;    // tokens a warp copies and works on at once; slices are multiples of it
-constexpr int kStages = 4;   // batches in flight per warp
+constexpr int kWarps = 8;       // warps per CTA
+constexpr int kMinLanes = 8;    // lanes of a row, at least
+constexpr int kBatchMax = 8;    // slices are multiples of it
 
 struct ScanParams {
   const void* in;      // x, or dh
@@ -48,11 +51,12 @@ struct ScanParams {
   float* last;         // final, or dh0 (may be null)
   const float* h0;     // backward: h_{-1} (may be null)
   const int* lens;     // may be null
-  float2* slices;      // [B][chunks * kWarps][groups * 32 V] (A, X) of each slice
-  float2* chunks;      // [B][chunks][groups * 32 V] of each chunk
+  float2* slices;      // [B][chunks * parts][width] (A, X) of each slice
+  float2* chunks;      // [B][chunks][width] of each chunk
   long long in_b, in_t, a_b, a_t, a_h, h_b, h_t, out_b, out_t, da_b, da_t, da_h;   // strides, elements
   int T, C, d;         // d: channels per gate (heads), or 1
-  int groups;          // channel groups of 32 V
+  int lanes;           // lanes per row: 8, 16 or 32
+  int groups;          // channel groups of lanes * V; width = groups * lanes * V
   int slice, nchunks;  // tokens per slice; chunks per sequence
 };
 
@@ -68,36 +72,113 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// V values of type T as one aligned access.
+// V values of type T, accessed 16 bytes at a time.
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
+struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
   T v[V];
+  __device__ __forceinline__ void widen(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f(v[i]);
+  }
+  __device__ __forceinline__ void round(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = from_f<T>(f[i]);
+  }
 };
+// A load that stays where it is written: the compiler would otherwise move each next to its use, to
+// save registers, and the loads of a batch would wait for one another.
+template <typename P>
+__device__ __forceinline__ P load_now(const void* src) {
+  P r;
+  if constexpr (sizeof(P) >= 16) {
+    uint4* w = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (size_t i = 0; i < sizeof(P) / 16; ++i)
+      asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "l"(static_cast<const uint4*>(src) + i));
+  } else if constexpr (sizeof(P) == 4) {
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(*reinterpret_cast<uint32_t*>(&r)) : "l"(src));
+  } else {
+    static_assert(sizeof(P) == 2);
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(*reinterpret_cast<uint16_t*>(&r)) : "l"(src));
+  }
+  return r;
+}
 
-// Copy one Pack from global to shared memory, or zeros where !ok (src is then not read, but is
-// inside the tensor). cp.async takes 4, 8 or 16 bytes; a 2-byte element goes through a register.
+// s = g s + x and a *= g, with the paired fp32 operations; one gate (GV = 1) or one per value.
+template <int V, int GV>
+__device__ __forceinline__ void advance(float (&s)[V], const float (&g)[GV], const float (&x)[V]) {
+  if constexpr (V == 1) {
+    s[0] = fmaf(g[0], s[0], x[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = __ffma2_rn(make_float2(g[GV == 1 ? 0 : i], g[GV == 1 ? 0 : i + 1]), make_float2(s[i], s[i + 1]),
+                                  make_float2(x[i], x[i + 1]));
+      s[i] = r.x;
+      s[i + 1] = r.y;
+    }
+  }
+}
+// s += g x.
+template <int V, int GV>
+__device__ __forceinline__ void accumulate(float (&s)[V], const float (&g)[GV], const float (&x)[V]) {
+  if constexpr (V == 1) {
+    s[0] = fmaf(g[0], x[0], s[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = __ffma2_rn(make_float2(g[GV == 1 ? 0 : i], g[GV == 1 ? 0 : i + 1]), make_float2(x[i], x[i + 1]),
+                                  make_float2(s[i], s[i + 1]));
+      s[i] = r.x;
+      s[i + 1] = r.y;
+    }
+  }
+}
+template <int GV>
+__device__ __forceinline__ void scale_by(float (&a)[GV], const float (&g)[GV]) {
+#pragma unroll
+  for (int i = 0; i < GV; ++i) a[i] *= g[i];
+}
+// A state moved past a pair.
+__device__ __forceinline__ float past(float2 pair, float s) { return fmaf(pair.x, s, pair.y); }
+
+// A store of data that this call does not read again: evict-first in L2.
+template <typename P>
+__device__ __forceinline__ void store_streaming(void* dst, const P& v) {
+  if constexpr (sizeof(P) >= 16) {
+#pragma unroll
+    for (size_t i = 0; i < sizeof(P) / 16; ++i)
+      __stcs(static_cast<uint4*>(dst) + i, reinterpret_cast<const uint4*>(&v)[i]);
+  } else if constexpr (sizeof(P) == 4) {
+    __stcs(static_cast<uint32_t*>(dst), *reinterpret_cast<const uint32_t*>(&v));
+  } else {
+    __stcs(static_cast<unsigned short*>(dst), *reinterpret_cast<const unsigned short*>(&v));
+  }
+}
+
+// 4 bytes, 16 or 32 from global to shared memory in the background; zeros where !ok, and then src,
+// though inside the tensor, is not read.
 template <typename P>
 __device__ __forceinline__ void copy_async(P* dst, const P* src, bool ok) {
-  if constexpr (sizeof(P) >= 4) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "n"(sizeof(P)), "r"(ok ? static_cast<uint32_t>(sizeof(P)) : 0u)
+  if constexpr (sizeof(P) == 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(ok ? 4u : 0u)
                  : "memory");
   } else {
-    P v = *src;
-    if (!ok) memset(&v, 0, sizeof v);
-    *dst = v;
+    static_assert(sizeof(P) % 16 == 0);
+#pragma unroll
+    for (uint32_t i = 0; i < sizeof(P) / 16; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst) + 16u * i),
+                   "l"(reinterpret_cast<uint64_t>(src) + 16 * i), "r"(ok ? 16u : 0u)
+                   : "memory");
   }
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
-// Bytes of the copy ring per warp: kStages batches of x (dh), the gates, and with kPrev of h.
-template <typename X, typename G, int V, bool kHead, bool kPrev>
-__host__ __device__ constexpr uint32_t ring_bytes() {
-  return kStages * kBatch * (32u * V * sizeof(X) * (kPrev ? 2 : 1) + (kHead ? 4u * 4u : 32u * V * sizeof(G)));
 }
 
 struct True {
@@ -107,180 +188,277 @@ struct False {
   static constexpr bool value = false;
 };
 
-// Where a warp works, and its stream of batches: token q of the scan is token q of the sequence
-// forward and token len - 1 - q backward. kPrev: h_{t-1} comes along (the backward apply).
+// The copy ring of a warp: kStages batches of kB tokens of x (dh), of the gates and, with kPrev, of
+// h, at most 9.75 KiB in all, so that two CTAs (their pairs included) fit an SM. Single elements
+// (V = 1) are loaded straight, 8 tokens at once: 16-bit ones are too small for cp.async, and 32-bit
+// ones cost less instructions this way (3 x 1561 tokens of 517 fp32 channels: 16 us, 29 us by ring).
+template <typename X, typename G, int V, bool kHead, bool kPrev>
+struct Ring {
+  static constexpr bool kUsed = V > 1;
+  static constexpr uint32_t kRowX = 32 * V * sizeof(X);
+  static constexpr uint32_t kRow = kRowX * (kPrev ? 2 : 1) + (kHead ? 32 : 32 * V * sizeof(G));
+  static constexpr int kB = V == 1 ? 8 : !kHead && kRow > 1024 ? 2 : 4;   // tokens worked on at once
+  static constexpr uint32_t kBatchG = kHead ? 32 * 4 : kB * 32 * V * sizeof(G);
+  static constexpr uint32_t kBatchBytes = kB * kRowX * (kPrev ? 2 : 1) + kBatchG;
+  static constexpr int kMost = 9984 / kBatchBytes;
+  static constexpr int kStages = kMost < 2 ? 2 : kMost > 8 ? 8 : kMost;
+  static constexpr uint32_t kBytes = kUsed ? kStages * kBatchBytes : 0;   // per warp
+};
+
+// kB tokens of a lane's channels: values, gates, and (kPrev) the states before them.
+template <typename PX, typename PG, int kB, bool kPrev>
+struct Batch {
+  PX x[kB], h[kPrev ? kB : 1];
+  PG g[kB];
+};
+
+// Where a thread works: token q of the scan is token q of the sequence forward and token
+// len - 1 - q backward.
 template <typename X, typename G, int V, bool kHead, bool kBack, bool kPrev>
 struct Place {
   static constexpr int GV = kHead ? 1 : V;   // gates per token a thread holds
+  using R = Ring<X, G, V, kHead, kPrev>;
+  static constexpr int kB = R::kB;
+  using B = Batch<Pack<X, V>, Pack<G, GV>, kB, kPrev>;
   using PX = Pack<X, V>;
   using PG = Pack<G, GV>;
-  int lane, warp, b, group, chunk, c, len;
+  int row_lane, part, parts, b, group, chunk, k, c, len;
   bool in_c;
-  int q0, end;         // this warp's slice: q0 <= q < end (empty behind the length)
+  int q0, batches;     // this slice's first token; batches with a token inside, over the warp
   const X* in;
   const G* ga;
   const X* hp;
-  PX* ring_x;          // [kStages][kBatch][32], this lane's entry of the first row
-  PX* ring_h;
-  PG* ring_g;          // the same; per head [kStages][4][kBatch], this lane's head of the first stage
-  G* copy_g;           // per head: where this lane copies a gate to (null: it copies none)
-  const G* from_g;     // and from, at token 0
-  // Chunks slowest, so that the CTAs in flight work on neighbouring tokens; the apply kernel
-  // takes them in reverse and begins with what the pairs kernel read last.
-  __device__ Place(const ScanParams& a, bool reverse, uint8_t* smem) {
-    lane = threadIdx.x & 31;
-    warp = threadIdx.x >> 5;
+  uint8_t* ring;       // this warp's
+  const G* head_ga;    // per head: the gates this lane copies (null: none)
+  // Chunks slowest, so that the CTAs in flight work on neighbouring tokens.
+  __device__ Place(const ScanParams& a, uint8_t* smem) {
+    row_lane = threadIdx.x & (a.lanes - 1);
+    part = threadIdx.x / a.lanes;
+    parts = blockDim.x / a.lanes;
     int u = blockIdx.x;
     group = u % a.groups;
     u /= a.groups;
     const int nb = gridDim.x / (a.groups * a.nchunks);
     b = u % nb;
-    chunk = reverse ? a.nchunks - 1 - u / nb : u / nb;
-    c = group * 32 * V + lane * V;
+    chunk = u / nb;
+    k = row_lane * V;                    // channel within the group
+    c = group * a.lanes * V + k;
     in_c = c < a.C;                      // V divides C, or V = 1
     const int cl = in_c ? c : 0;         // lanes behind the last channel stay inside the tensor
     len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-    q0 = (chunk * (blockDim.x >> 5) + warp) * a.slice;
-    end = min(q0 + a.slice, len);
+    q0 = (chunk * parts + part) * a.slice;
+    batches = __reduce_max_sync(0xffffffffu, max(0, (min(q0 + a.slice, len) - q0 + kB - 1) / kB));
     in = static_cast<const X*>(a.in) + b * a.in_b + cl;
     ga = static_cast<const G*>(a.a) + b * a.a_b + (kHead ? (cl / a.d) * a.a_h : static_cast<long long>(cl));
     hp = kPrev ? static_cast<const X*>(a.hprev) + b * a.h_b + cl : nullptr;
-    uint8_t* ring = smem + warp * ring_bytes<X, G, V, kHead, kPrev>();
-    ring_x = reinterpret_cast<PX*>(ring) + lane;
-    ring += kStages * kBatch * 32 * sizeof(PX);
-    ring_h = reinterpret_cast<PX*>(ring) + lane;
-    if (kPrev) ring += kStages * kBatch * 32 * sizeof(PX);
-    copy_g = nullptr;
-    from_g = nullptr;
-    if constexpr (kHead) {   // lane l copies the gate of token l % kBatch and head l / kBatch of the group's
-      const int h0 = group * 32 * V / a.d, h = lane / kBatch;
-      ring_g = reinterpret_cast<PG*>(ring) + (c / a.d - h0) * kBatch;
-      if (h < 32 * V / a.d && h0 + h < a.C / a.d) {
-        copy_g = reinterpret_cast<G*>(ring) + lane;
-        from_g = static_cast<const G*>(a.a) + b * a.a_b + (h0 + h) * a.a_h;
-      }
-    } else {
-      ring_g = reinterpret_cast<PG*>(ring) + lane;
+    ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    head_ga = nullptr;
+    if constexpr (kHead) {   // lane l of a row copies the gate of token l % kB and head l / kB of the group's
+      const int head = group * a.lanes * V / a.d + row_lane / kB;
+      if (row_lane / kB < a.lanes * V / a.d && head < a.C / a.d)
+        head_ga = static_cast<const G*>(a.a) + b * a.a_b + head * a.a_h;
     }
   }
   __device__ int token(int q) const { return kBack ? len - 1 - q : q; }
-  // Start copying tokens q .. q + kBatch - 1 to a stage: one group, empty behind the slice.
-  __device__ void copy(const ScanParams& a, int q, int stage) const {
-    if (q < end) {
+  __device__ PX* ring_x(int stage, int i) const {
+    return reinterpret_cast<PX*>(ring + stage * R::kBatchBytes + i * R::kRowX) + (threadIdx.x & 31);
+  }
+  __device__ PX* ring_h(int stage, int i) const {
+    return reinterpret_cast<PX*>(ring + stage * R::kBatchBytes + (kB + i) * R::kRowX) + (threadIdx.x & 31);
+  }
+  __device__ uint8_t* ring_g(int stage) const {
+    return ring + stage * R::kBatchBytes + kB * R::kRowX * (kPrev ? 2 : 1);
+  }
+  // The slice's batches are worked on in order (kReverse: from the last to the first). Start copying
+  // the j-th of them to its stage: one group, empty behind the last.
+  template <bool kReverse>
+  __device__ __forceinline__ void copy(const ScanParams& a, int j) const {
+    if constexpr (R::kUsed) {
+      const int q = q0 + (kReverse ? batches - 1 - j : j) * kB, stage = j % R::kStages;
+      if (j >= batches || q >= len) {
+        // nothing
+      } else if ((!kBack || q > 0) && q + kB + (kBack ? 1 : 0) <= len) {   // all inside: no clamping
+        const int t0 = token(q);
+        const X* px = in + t0 * a.in_t;
+        const G* pg = ga + (kBack ? t0 + 1 : t0) * a.a_t;
+        const X* ph = kPrev ? hp + (t0 - 1) * a.h_t : nullptr;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const bool ok = in_c && q + i < len;
-        const int t = ok ? token(q + i) : 0, tg = kBack ? min(t + 1, len - 1) : t;
-        copy_async(ring_x + (stage * kBatch + i) * 32, reinterpret_cast<const PX*>(in + t * a.in_t), ok);
-        if constexpr (!kHead)
-          copy_async(ring_g + (stage * kBatch + i) * 32, reinterpret_cast<const PG*>(ga + tg * a.a_t), ok);
-        if constexpr (kPrev)
-          copy_async(ring_h + (stage * kBatch + i) * 32, reinterpret_cast<const PX*>(hp + max(t - 1, 0) * a.h_t),
-                     ok && t > 0);
+        for (int i = 0; i < kB; ++i) {
+          copy_async(ring_x(stage, i), reinterpret_cast<const PX*>(px), true);
+          px = kBack ? px - a.in_t : px + a.in_t;
+          if constexpr (!kHead) {
+            copy_async(reinterpret_cast<PG*>(ring_g(stage)) + i * 32 + (threadIdx.x & 31),
+                       reinterpret_cast<const PG*>(pg), true);
+            pg = kBack ? pg - a.a_t : pg + a.a_t;
+          }
+          if constexpr (kPrev) {
+            copy_async(ring_h(stage, i), reinterpret_cast<const PX*>(ph), true);
+            ph -= a.h_t;
+          }
+        }
+        if constexpr (kHead) {
+          if (head_ga)
+            copy_async(reinterpret_cast<G*>(ring_g(stage)) + (threadIdx.x & 31),
+                       head_ga + (token(q + row_lane % kB) + (kBack ? 1 : 0)) * a.a_t, true);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const bool ok = q + i < len && in_c;
+          const int t = max(token(q + i), 0), tl = min(t, len - 1);
+          copy_async(ring_x(stage, i), reinterpret_cast<const PX*>(in + tl * a.in_t), ok);
+          if constexpr (!kHead)
+            copy_async(reinterpret_cast<PG*>(ring_g(stage)) + i * 32 + (threadIdx.x & 31),
+                       reinterpret_cast<const PG*>(ga + (kBack ? min(tl + 1, len - 1) : tl) * a.a_t), ok);
+          if constexpr (kPrev)
+            copy_async(ring_h(stage, i), reinterpret_cast<const PX*>(hp + max(tl - 1, 0) * a.h_t), ok && t > 0);
+        }
+        if constexpr (kHead) {
+          const int qi = q + row_lane % kB, t = min(max(token(qi), 0) + (kBack ? 1 : 0), len - 1);
+          if (head_ga)
+            copy_async(reinterpret_cast<G*>(ring_g(stage)) + (threadIdx.x & 31), head_ga + t * a.a_t, qi < len);
+        }
       }
-      if constexpr (kHead) {
-        const int i = lane % kBatch;
-        const int t = min(token(q + i) + (kBack ? 1 : 0), len - 1);
-        if (copy_g)
-          copy_async(reinterpret_cast<Pack<G, 1>*>(copy_g + stage * kBatch * 4),
-                     reinterpret_cast<const Pack<G, 1>*>(from_g + max(t, 0) * a.a_t), q + i < len);
-      }
+      copy_commit();
     }
-    copy_commit();
   }
-  __device__ void start(const ScanParams& a) const {
+  template <bool kReverse>
+  __device__ __forceinline__ void start(const ScanParams& a) const {
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) copy(a, q0 + k * kBatch, k);
+    for (int j = 0; j < R::kStages; ++j) copy<kReverse>(a, j);
   }
-  // After start(): call work(exact, q, stage) for each batch of the slice in order. exact is
-  // False where a token of the batch lies behind the length or, backward, is the last one:
-  // there the gate is not what the ring holds but 1, so that a state passes unchanged (the
-  // value is 0) and dfinal reaches the last token undamped.
-  template <typename Work>
-  __device__ void stream(const ScanParams& a, Work&& work) const {
-    int stage = 0;
-    for (int q = q0; q < end; q += kBatch) {
-      copy_wait<kStages - 1>();
-      if (kHead) __syncwarp();   // gates are copied by other lanes than those that read them
-      if (q + kBatch > len || (kBack && q == 0))
-        work(False{}, q, stage);
-      else
-        work(True{}, q, stage);
+  // After start(): work(inner, q, batch) for each batch of the slice, by whole warps.
+  // inner is True where all of the batch, and of its neighbours, is inside the sequence.
+  // Elsewhere what lies behind the length has value 0 and gate 1, so that a state passes
+  // unchanged; backward, the last token's gate is 1 too (dfinal reaches it undamped).
+  template <bool kReverse, typename Work>
+  __device__ __forceinline__ void stream(const ScanParams& a, Work&& work) const {
+    for (int j = 0; j < batches; ++j) {
+      const int q = q0 + (kReverse ? batches - 1 - j : j) * kB;
+      const bool inner = __all_sync(0xffffffffu, (!kBack || q > 0) && q + kB + (kBack ? 1 : 0) <= len);
+      B r;
+      if constexpr (R::kUsed) {
+        const int stage = j % R::kStages;
+        copy_wait<R::kStages - 1>();
+        if (kHead) __syncwarp();   // gates are copied by other lanes than those that read them
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          r.x[i] = *ring_x(stage, i);
+          if constexpr (kPrev) r.h[i] = *ring_h(stage, i);
+          if constexpr (kHead)   // this row's lanes, its head, its token
+            r.g[i].v[0] = reinterpret_cast<const float*>(ring_g(stage))[(threadIdx.x & 31 & ~(a.lanes - 1)) +
+                                                                        row_lane * V / a.d * kB + i];
+          else
+            r.g[i] = reinterpret_cast<const PG*>(ring_g(stage))[i * 32 + (threadIdx.x & 31)];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const int t = max(token(q + i), 0), tl = min(t, len - 1);
+          r.x[i] = load_now<PX>(in + tl * a.in_t);
+          r.g[i] = load_now<PG>(ga + (kBack ? min(tl + 1, len - 1) : tl) * a.a_t);
+          if constexpr (kPrev) r.h[i] = load_now<PX>(hp + max(tl - 1, 0) * a.h_t);
+        }
+      }
+      if (inner) {
+        work(True{}, q, r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const bool ok = q + i < len, gok = ok && (!kBack || q + i > 0);
+#pragma unroll
+          for (int v = 0; v < V; ++v) r.x[i].v[v] = ok ? r.x[i].v[v] : from_f<X>(0.f);
+#pragma unroll
+          for (int v = 0; v < GV; ++v) r.g[i].v[v] = gok ? r.g[i].v[v] : from_f<G>(1.f);
+        }
+        work(False{}, q, r);
+      }
       if (kHead) __syncwarp();
-      copy(a, q + kStages * kBatch, stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      copy<kReverse>(a, j + R::kStages);
     }
   }
-  __device__ PX value(int stage, int i) const { return ring_x[(stage * kBatch + i) * 32]; }
-  __device__ PX prev(int stage, int i) const { return ring_h[(stage * kBatch + i) * 32]; }
-  template <bool kExact>
-  __device__ void gates(int q, int stage, int i, float (&g)[GV]) const {
-    const PG p = kHead ? ring_g[stage * kBatch * 4 + i] : ring_g[(stage * kBatch + i) * 32];
-    const bool ok = kExact || (q + i < len && (!kBack || q + i > 0));
+  // The (A, X) of this slice, after start<true>(): from the end, X = sum of x times the gates behind.
+  __device__ __forceinline__ void pairs(const ScanParams& a, float2 (&pair)[V]) const {
+    float A[GV], S[V];
 #pragma unroll
-    for (int v = 0; v < GV; ++v) g[v] = ok ? to_f(p.v[v]) : 1.f;
-  }
-  // The (A, X) of this warp's slice (after start()).
-  __device__ void pairs(const ScanParams& a, float (&A)[V], float (&S)[V]) const {
-    float Ag[GV];
-#pragma unroll
-    for (int v = 0; v < GV; ++v) Ag[v] = 1.f;
+    for (int v = 0; v < GV; ++v) A[v] = 1.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) S[v] = 0.f;
-    stream(a, [&](auto exact, int q, int stage) {
+    stream<true>(a, [&](auto, int, const B& r) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        float g[GV];
-        gates<decltype(exact)::value>(q, stage, i, g);
-        const PX x = value(stage, i);
-#pragma unroll
-        for (int v = 0; v < V; ++v) S[v] = fmaf(g[kHead ? 0 : v], S[v], to_f(x.v[v]));
-#pragma unroll
-        for (int v = 0; v < GV; ++v) Ag[v] *= g[v];
+      for (int i = kB - 1; i >= 0; --i) {
+        float xf[V], gf[GV];
+        r.x[i].widen(xf);
+        r.g[i].widen(gf);
+        accumulate(S, A, xf);
+        scale_by(A, gf);
       }
     });
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = Ag[kHead ? 0 : v];
+    for (int v = 0; v < V; ++v) pair[v] = make_float2(A[kHead ? 0 : v], S[v]);
   }
 };
 
-template <typename X, typename G, int V, bool kHead, bool kBack>
-__global__ void __launch_bounds__(32 * kWarps, V == 4 && !(kHead && kBack) ? 2 : 1)
-    arl2_scan_pairs_kernel(const __grid_constant__ ScanParams a) {
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 s_pair[kWarps][32 * V];
-  griddep_launch_dependents();
-  const Place<X, G, V, kHead, kBack, false> p(a, false, ring);
-  float A[V], S[V];
-  p.start(a);
-  p.pairs(a, A, S);
-  const long long width = static_cast<long long>(a.groups) * 32 * V;
-  const int c = p.group * 32 * V + p.lane * V;
-  float2* dst = a.slices + ((static_cast<long long>(p.b) * a.nchunks + p.chunk) * kWarps + p.warp) * width + c;
+// A row of pairs, V of them per lane.
+template <int V>
+__device__ __forceinline__ void load_pairs(const float2* src, float2 (&r)[V]) {
+  if constexpr (V == 1) {
+    r[0] = src[0];
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    dst[v] = make_float2(A[v], S[v]);
-    s_pair[p.warp][p.lane * V + v] = make_float2(A[v], S[v]);
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < 32 * V; k += blockDim.x) {
-    float2 r = s_pair[0][k];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      const float2 n = s_pair[w][k];
-      r = make_float2(r.x * n.x, fmaf(n.x, r.y, n.y));
+    for (int v = 0; v < V; v += 2) {
+      const float4 p = *reinterpret_cast<const float4*>(src + v);
+      r[v] = make_float2(p.x, p.y);
+      r[v + 1] = make_float2(p.z, p.w);
     }
-    a.chunks[(static_cast<long long>(p.b) * a.nchunks + p.chunk) * width + p.group * 32 * V + k] = r;
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_pairs(float2* dst, const float2 (&r)[V]) {
+  if constexpr (V == 1) {
+    dst[0] = r[0];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<float4*>(dst + v) = make_float4(r[v].x, r[v].y, r[v + 1].x, r[v + 1].y);
   }
 }
 
-// Sums of kBatch values over the lanes of a head (d / 4 of them: 8, 16 or 32), by halving the
-// values held: each exchange sends the half that the partner keeps. Lane l of a head ends with
-// the sum of value (l / same) % kBatch, which `same` = lanes / kBatch neighbouring lanes hold.
-__device__ __forceinline__ float head_sums(float (&r)[kBatch], int lanes, int lane, int* index) {
+template <typename X, typename G, int V, bool kHead, bool kBack>
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    arl2_scan_pairs_kernel(const __grid_constant__ ScanParams a) {
+  __shared__ __align__(16) float2 s_pair[kWarps * 32 * V];   // [parts][lanes V]
+  extern __shared__ __align__(16) uint8_t ring[];
+  griddep_launch_dependents();
+  const Place<X, G, V, kHead, kBack, false> p(a, ring);
+  float2 r[V];
+  p.template start<true>(a);
+  p.pairs(a, r);
+  const int wide = a.lanes * V;
+  const long long width = static_cast<long long>(a.groups) * wide;
+  const long long row = static_cast<long long>(p.b) * a.nchunks + p.chunk;
+  store_pairs(a.slices + (row * p.parts + p.part) * width + p.group * wide + p.k, r);
+  store_pairs(s_pair + p.part * wide + p.k, r);
+  __syncthreads();
+  for (int k = threadIdx.x; k < wide; k += blockDim.x) {
+    float2 n = s_pair[k];
+#pragma unroll 4
+    for (int w = 1; w < p.parts; ++w) {
+      const float2 m = s_pair[w * wide + k];
+      n = make_float2(n.x * m.x, past(m, n.y));
+    }
+    a.chunks[row * width + p.group * wide + k] = n;
+  }
+}
+
+// Sums of kB values over the lanes of a head (d / V of them, a power of two >= kB), by halving
+// the values held: each exchange sends the half that the partner keeps. Lane l of a head ends
+// with the sum of value l / same % kB, which `same` = lanes / kB neighbouring lanes hold.
+template <int kB>
+__device__ __forceinline__ float head_sums(float (&r)[kB], int lanes, int lane, int* index) {
   int m = lanes >> 1;
 #pragma unroll
-  for (int n = kBatch / 2; n >= 1; n >>= 1, m >>= 1) {
+  for (int n = kB / 2; n >= 1; n >>= 1, m >>= 1) {
     const bool upper = (lane & m) != 0;   // keeps the upper half of the values
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -289,148 +467,134 @@ __device__ __forceinline__ float head_sums(float (&r)[kBatch], int lanes, int la
     }
   }
   for (; m > 0; m >>= 1) r[0] += __shfl_xor_sync(0xffffffffu, r[0], m);
-  *index = lane / (lanes / kBatch) % kBatch;
+  *index = lane / (lanes / kB) % kB;
   return r[0];
 }
 
 template <typename X, typename G, int V, bool kHead, bool kBack>
-__global__ void __launch_bounds__(32 * kWarps, V == 4 && !(kHead && kBack) ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarps, 2)
     arl2_scan_apply_kernel(const __grid_constant__ ScanParams a) {
   using P = Place<X, G, V, kHead, kBack, kBack>;
   using PX = typename P::PX;
   using PG = typename P::PG;
-  constexpr int GV = P::GV;
-  __shared__ float2 s_pair[kWarps][32 * V];    // each warp's share of the earlier chunks
-  __shared__ float2 s_slice[kWarps][32 * V];   // the chunk's slices
+  constexpr int GV = P::GV, kB = P::kB;
+  __shared__ __align__(16) float2 s_pair[kWarps * 32 * V];    // each part's share of the earlier chunks
+  __shared__ __align__(16) float2 s_slice[kWarps * 32 * V];   // the chunk's slices
   extern __shared__ __align__(16) uint8_t ring[];
-  const P p(a, true, ring);
-  const int lane = p.lane, warp = p.warp, len = p.len, W = blockDim.x >> 5;
-  p.start(a);   // in flight while the state it starts from is composed
+  const P p(a, ring);
+  const bool single = a.nchunks == 1 && p.parts > 1;   // the slices' pairs are made here
+  if (single)
+    p.template start<true>(a);
+  else
+    p.template start<false>(a);   // in flight while the state it starts from is composed
+  const int len = p.len, wide = a.lanes * V;
   float state[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) state[v] = a.init && p.in_c ? a.init[static_cast<long long>(p.b) * a.C + p.c + v] : 0.f;
 
-  // The state this warp's slice starts from: every warp brings its slice's pair and composes its
-  // share of the earlier chunks; all meet in shared memory.
-  float A[V], S[V];
-  if (a.nchunks == 1) {
-    if (W > 1) {
-      p.pairs(a, A, S);
-      p.start(a);
-#pragma unroll
-      for (int v = 0; v < V; ++v) s_slice[warp][lane * V + v] = make_float2(A[v], S[v]);
-    }
-  } else {
+  // The state this slice starts from: every part brings its slice's pair and composes its share
+  // of the earlier chunks; all meet in shared memory.
+  if (single) {
+    float2 own[V];
+    p.pairs(a, own);
+    p.template start<false>(a);
+    store_pairs(s_slice + p.part * wide + p.k, own);
+  } else if (a.nchunks > 1) {
     griddep_wait();   // the pairs kernel's results
-    const long long width = static_cast<long long>(a.groups) * 32 * V;
-    const float2* mine =
-        a.slices + ((static_cast<long long>(p.b) * a.nchunks + p.chunk) * kWarps + warp) * width + p.group * 32 * V;
-    Pack<float2, V> own;
+    const long long width = static_cast<long long>(a.groups) * wide;
+    const long long row = static_cast<long long>(p.b) * a.nchunks;
+    float2 own[V], sum[V];
+    load_pairs(a.slices + ((row + p.chunk) * p.parts + p.part) * width + p.group * wide + p.k, own);
+    const int share = (p.chunk + p.parts - 1) / p.parts;
+    const int k0 = min(p.part * share, p.chunk), k1 = min(k0 + share, p.chunk);
 #pragma unroll
-    for (int v = 0; v < V; ++v) own.v[v] = mine[lane * V + v];
-    const int share = (p.chunk + kWarps - 1) / kWarps;
-    const int k0 = min(warp * share, p.chunk), k1 = min(k0 + share, p.chunk);
+    for (int v = 0; v < V; ++v) sum[v] = make_float2(1.f, 0.f);
+    const float2* src = a.chunks + (row + k0) * width + p.group * wide + p.k;
+#pragma unroll 2
+    for (int i = k0; i < k1; ++i, src += width) {
+      float2 n[V];
+      load_pairs(src, n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, S[v] = 0.f;
-    const float2* src =
-        a.chunks + (static_cast<long long>(p.b) * a.nchunks + k0) * width + p.group * 32 * V + lane * V;
-    for (int k = k0; k < k1; k += 4) {
-      Pack<float2, V> n[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) n[i].v[v] = src[min(k - k0 + i, k1 - 1 - k0) * width + v];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (k + i < k1) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            S[v] = fmaf(n[i].v[v].x, S[v], n[i].v[v].y);
-            A[v] *= n[i].v[v].x;
-          }
-        }
+      for (int v = 0; v < V; ++v) sum[v] = make_float2(sum[v].x * n[v].x, past(n[v], sum[v].y));
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s_pair[warp][lane * V + v] = make_float2(A[v], S[v]);
-      s_slice[warp][lane * V + v] = own.v[v];
-    }
+    store_pairs(s_pair + p.part * wide + p.k, sum);
+    store_pairs(s_slice + p.part * wide + p.k, own);
   }
-  if (W > 1) {
+  if (p.parts > 1) {
     __syncthreads();
     if (a.nchunks > 1) {
+#pragma unroll 2
+      for (int w = 0; w < p.parts; ++w) {
+        float2 n[V];
+        load_pairs(s_pair + w * wide + p.k, n);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float2 n = s_pair[w][lane * V + v];
-          state[v] = fmaf(n.x, state[v], n.y);
-        }
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < warp) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float2 n = s_slice[w][lane * V + v];
-          state[v] = fmaf(n.x, state[v], n.y);
-        }
+        for (int v = 0; v < V; ++v) state[v] = past(n[v], state[v]);
       }
+    }
+#pragma unroll 2
+    for (int w = 0; w < p.part; ++w) {
+      float2 n[V];
+      load_pairs(s_slice + w * wide + p.k, n);
+#pragma unroll
+      for (int v = 0; v < V; ++v) state[v] = past(n[v], state[v]);
+    }
   }
 
   X* out = static_cast<X*>(a.out) + p.b * a.out_b + p.c;
-  G* da = kBack ? static_cast<G*>(a.da) + p.b * a.da_b + (kHead ? 0 : static_cast<long long>(p.c)) : nullptr;
-  const int head = kHead ? p.c / a.d : 0;
-  float first[kBack ? V : 1];   // backward: h_{-1}
-  if constexpr (kBack) {
+  G* da = kBack ? static_cast<G*>(a.da) + p.b * a.da_b + (kHead ? (p.c / a.d) * a.da_h : static_cast<long long>(p.c))
+                : nullptr;
+  p.template stream<false>(a, [&](auto inner, int q, const typename P::B& r) {
+    constexpr bool kInner = decltype(inner)::value;
+    const int t0 = p.token(q);
+    X* po = out + t0 * a.out_t;
+    [[maybe_unused]] G* pa = kBack && !kHead ? da + t0 * a.da_t : nullptr;
+    [[maybe_unused]] float sums[kB];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      first[v] = a.h0 && p.in_c ? a.h0[static_cast<long long>(p.b) * a.C + p.c + v] : 0.f;
-  }
-  p.stream(a, [&](auto exact, int q, int stage) {
-    [[maybe_unused]] float sums[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const bool ok = (decltype(exact)::value || q + i < len) && p.in_c;
-      const int t = p.token(q + i);
-      float g[GV];
-      p.template gates<decltype(exact)::value>(q, stage, i, g);
-      const PX x = p.value(stage, i);
+    for (int i = 0; i < kB; ++i) {
+      const bool ok = (kInner || q + i < len) && p.in_c;
+      float xf[V], gf[GV];
+      r.x[i].widen(xf);
+      r.g[i].widen(gf);
+      advance(state, gf, xf);
       PX o;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        state[v] = fmaf(g[kHead ? 0 : v], state[v], to_f(x.v[v]));
-        o.v[v] = from_f<X>(state[v]);
-      }
-      if (ok) *reinterpret_cast<PX*>(out + t * a.out_t) = o;
+      o.round(state);
+      if (ok) store_streaming(po, o);
+      po = kBack ? po - a.out_t : po + a.out_t;
       if constexpr (kBack) {
-        const PX h = p.prev(stage, i);
-        float prod[V];
+        float hf[V];
+        r.h[i].widen(hf);
+        if constexpr (!kInner) {
+          if (p.token(q + i) <= 0) {   // h_{-1}
 #pragma unroll
-        for (int v = 0; v < V; ++v) prod[v] = state[v] * (t > 0 ? to_f(h.v[v]) : first[v]);
+            for (int v = 0; v < V; ++v)
+              hf[v] = a.h0 && p.in_c ? a.h0[static_cast<long long>(p.b) * a.C + p.c + v] : 0.f;
+          }
+        }
         if constexpr (kHead) {
-          float sum = prod[0];
+          float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int v = 1; v < V; ++v) sum += prod[v];
-          sums[i] = sum;
+          for (int v = 0; v < V; v += 2)
+            s = __ffma2_rn(make_float2(state[v], state[v + 1]), make_float2(hf[v], hf[v + 1]), s);
+          sums[i] = s.x + s.y;
         } else {
           PG o2;
 #pragma unroll
-          for (int v = 0; v < GV; ++v) o2.v[v] = from_f<G>(prod[v]);
-          if (ok) *reinterpret_cast<PG*>(da + t * a.da_t) = o2;
+          for (int v = 0; v < GV; ++v) o2.v[v] = from_f<G>(state[v] * hf[v]);
+          if (ok) store_streaming(pa, o2);
+          pa -= a.da_t;
         }
       }
     }
     if constexpr (kBack && kHead) {
       const int lanes = a.d / V;
       int i = 0;
-      const float sum = head_sums(sums, lanes, lane, &i);
-      const bool writer = p.in_c && lane % (lanes / kBatch) == 0;   // one of the lanes that hold it
-      if (writer && q + i < len) da[head * a.da_h + p.token(q + i) * a.da_t] = from_f<G>(sum);
+      const float sum = head_sums(sums, lanes, threadIdx.x & 31, &i);
+      const bool writer = p.in_c && p.row_lane % (lanes / kB) == 0;   // one of the lanes that hold it
+      if (writer && (kInner || q + i < len)) da[p.token(q + i) * a.da_t] = from_f<G>(sum);
     }
   });
 
-  // The warp whose slice holds the last token (the first slice, of an empty sequence) has the
+  // The part whose slice holds the last token (the first slice, of an empty sequence) has the
   // final state.
   if (a.last && p.in_c && (len > 0 ? p.q0 < len && p.q0 + a.slice >= len : p.q0 == 0)) {
 #pragma unroll
@@ -439,14 +603,14 @@ __global__ void __launch_bounds__(32 * kWarps, V == 4 && !(kHead && kBack) ? 2 :
       a.last[static_cast<long long>(p.b) * a.C + p.c + v] = g * state[v];
     }
   }
-  // Behind the length: zeros (each warp in its own slice's place).
+  // Behind the length: zeros (each part in its own slice's place).
   for (int t = max(p.q0, len); t < min(p.q0 + a.slice, a.T); ++t) {
     PX z;
 #pragma unroll
     for (int v = 0; v < V; ++v) z.v[v] = from_f<X>(0.f);
     if (p.in_c) *reinterpret_cast<PX*>(out + t * a.out_t) = z;
     if constexpr (kBack && kHead) {
-      if (p.in_c && p.c % a.d == 0) da[head * a.da_h + t * a.da_t] = from_f<G>(0.f);
+      if (p.in_c && p.c % a.d == 0) da[t * a.da_t] = from_f<G>(0.f);
     } else if constexpr (kBack) {
       PG gz;
 #pragma unroll
@@ -456,33 +620,40 @@ __global__ void __launch_bounds__(32 * kWarps, V == 4 && !(kHead && kBack) ? 2 :
   }
 }
 
-// How a call is cut. Slices are as long as they can be while there are four CTAs for every SM
-// of a B200 (kFill), since shorter ones mean more pairs to write and compose: between 8 and 64
-// tokens, longer only where a sequence would have more than 256 chunks (each CTA composes all
-// the chunks before its own). A sequence of at most kWarps 64-token slices is one chunk, cut into no
-// more warps than it has batches.
+// How a call is cut. The CTAs are to fill the GPU once, two for each SM of a B200: more would mean more pairs
+// to write and to compose (each CTA composes all the chunks before its own), fewer leave SMs
+// idle (without the ring, twice as many: their loads are hidden by other warps alone). So chunks are as many as that allows, at most 256 a sequence, in slices of 8 tokens or
+// more. A sequence of at most one chunk of 64-token slices is one chunk, cut into no more parts
+// than it has batches.
 struct ScanPlan {
-  int groups, slice, nchunks, warps;
+  int lanes, groups, slice, nchunks, warps;
   size_t slice_pairs, chunk_pairs;   // workspace, in (A, X) pairs
 };
-constexpr int kFill = 4 * 148;
 ScanPlan plan_scan(int B, int T, int C, int V) {
   ScanPlan p{};
-  p.groups = (C + 32 * V - 1) / (32 * V);
+  p.lanes = 32;
+  while (p.lanes > kMinLanes && (p.lanes / 2) * V >= C) p.lanes /= 2;
+  p.groups = (C + p.lanes * V - 1) / (p.lanes * V);
+  const int per_warp = 32 / p.lanes, parts = kWarps * per_warp;
   const long long units = static_cast<long long>(B) * p.groups;
-  auto chunks = [&](long long slice) { return (T + kWarps * slice - 1) / (kWarps * slice); };
+  auto chunks = [&](long long slice) { return (T + parts * slice - 1) / (parts * slice); };
   long long slice = 64;
-  while (slice > 8 && chunks(slice) > 1 && units * chunks(slice) < kFill) slice /= 2;
-  while (chunks(slice) > 256) slice *= 2;
+  if (chunks(slice) > 1) {
+    const long long fill = (V > 1 ? 2 : 4) * 148;
+    const long long want = std::min<long long>(256, std::max<long long>(1, fill / units));
+    slice = (T + parts * want - 1) / (parts * want);
+    slice = std::max<long long>(kBatchMax, (slice + kBatchMax - 1) / kBatchMax * kBatchMax);
+  }
   p.nchunks = static_cast<int>(chunks(slice));
   p.warps = kWarps;
   if (p.nchunks == 1) {
-    p.warps = std::max(1, std::min(kWarps, T / kBatch));
-    slice = ((T + p.warps - 1) / p.warps + kBatch - 1) / kBatch * kBatch;
+    p.warps = std::max(1, std::min(kWarps, T / (kBatchMax * per_warp)));
+    const int n = p.warps * per_warp;
+    slice = ((T + n - 1) / n + kBatchMax - 1) / kBatchMax * kBatchMax;
   } else {
-    const size_t width = static_cast<size_t>(p.groups) * 32 * V;
+    const size_t width = static_cast<size_t>(p.groups) * p.lanes * V;
     p.chunk_pairs = static_cast<size_t>(B) * p.nchunks * width;
-    p.slice_pairs = p.chunk_pairs * kWarps;
+    p.slice_pairs = p.chunk_pairs * parts;
   }
   p.slice = static_cast<int>(slice);
   return p;
@@ -492,6 +663,7 @@ template <typename X, typename G, int V, bool kHead, bool kBack>
 cudaError_t launch(const ScanParams& p, int B, int dev, void* workspace, cudaStream_t st) {
   const ScanPlan plan = plan_scan(B, p.T, p.C, V);
   ScanParams a = p;
+  a.lanes = plan.lanes;
   a.groups = plan.groups;
   a.slice = plan.slice;
   a.nchunks = plan.nchunks;
@@ -499,42 +671,41 @@ cudaError_t launch(const ScanParams& p, int B, int dev, void* workspace, cudaStr
   a.chunks = a.slices + plan.slice_pairs;
   const long long ctas = static_cast<long long>(B) * plan.groups * plan.nchunks;
   if (ctas > INT_MAX) return cudaErrorInvalidConfiguration;
+  auto* pairs = &arl2_scan_pairs_kernel<X, G, V, kHead, kBack>;
+  auto* apply = &arl2_scan_apply_kernel<X, G, V, kHead, kBack>;
+  constexpr uint32_t kPairsRing = Ring<X, G, V, kHead, false>::kBytes, kApplyRing = Ring<X, G, V, kHead, kBack>::kBytes;
+  static std::atomic<unsigned long long> allowed{0};   // devices that were told of the rings, by bit
+  if (!(allowed.load(std::memory_order_acquire) >> dev & 1)) {
+    cudaError_t e = cudaFuncSetAttribute(pairs, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kPairsRing);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(apply, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kApplyRing);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(1ull << dev, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(32 * plan.warps);
   cfg.stream = st;
-  auto* pairs = &arl2_scan_pairs_kernel<X, G, V, kHead, kBack>;
-  auto* apply = &arl2_scan_apply_kernel<X, G, V, kHead, kBack>;
-  constexpr uint32_t kPairsRing = kWarps * ring_bytes<X, G, V, kHead, false>();
-  constexpr uint32_t kApplyRing = kWarps * ring_bytes<X, G, V, kHead, kBack>();
-  cudaError_t e = cudaSuccess;
-  static std::atomic<unsigned long long> allowed{0};   // devices that were told, by bit
-  if (!(allowed.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(pairs, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPairsRing));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(apply, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kApplyRing));
-    if (e != cudaSuccess) return e;
-    allowed.fetch_or(1ull << dev, std::memory_order_release);
-  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 0;
   if (plan.nchunks > 1) {
-    cfg.dynamicSmemBytes = kPairsRing;
-    e = cudaLaunchKernelEx(&cfg, pairs, a);
+    cfg.dynamicSmemBytes = kWarps * kPairsRing;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, pairs, a);
     if (e != cudaSuccess) return e;
     cfg.numAttrs = 1;
   }
-  cfg.dynamicSmemBytes = kApplyRing / kWarps * plan.warps;
+  cfg.dynamicSmemBytes = plan.warps * kApplyRing;
   return cudaLaunchKernelEx(&cfg, apply, a);
 }
 
 template <typename X, typename G, bool kBack>
 cudaError_t by_width(const ScanParams& p, int B, int dev, void* ws, bool head, bool wide, cudaStream_t st) {
-  if (head) return launch<X, float, 4, true, kBack>(p, B, dev, ws, st);
-  return wide ? launch<X, G, 4, false, kBack>(p, B, dev, ws, st) : launch<X, G, 1, false, kBack>(p, B, dev, ws, st);
+  constexpr int V = 16 / sizeof(X);
+  if (head) return launch<X, float, V, true, kBack>(p, B, dev, ws, st);
+  return wide ? launch<X, G, V, false, kBack>(p, B, dev, ws, st) : launch<X, G, 1, false, kBack>(p, B, dev, ws, st);
 }
 
 template <bool kBack>
@@ -561,8 +732,8 @@ Strides strides_of(const int64_t* s, const arl2_scan_shape& shape, bool gates = 
   return {shape.B > 1 ? s[0] : 0, shape.T > 1 ? s[1] : 0, gates && shape.heads > 1 ? s[2] : 0};
 }
 
-// A [B, T, C] tensor, unit channel stride: whether its strides are in range, and whether groups
-// of 4 channels of it can be accessed at once. An output's elements must not share memory.
+// A [B, T, C] tensor, unit channel stride: whether its strides are in range, and whether 16 bytes
+// of it can be accessed at once. An output's elements must not share memory.
 bool strides_ok(const Strides& x, int B, int T, int C, bool output) {
   const long long sb = x.b, st = x.t;
   if (sb < 0 || st < 0 || x.h < 0) return false;
@@ -571,7 +742,10 @@ bool strides_ok(const Strides& x, int B, int T, int C, bool output) {
   if (B > 1 && sb < (T > 1 ? (T - 1) * st : 0) + C && !(sb >= C && T > 1 && st >= (B - 1) * sb + C)) return false;
   return true;
 }
-bool wide_ok(const void* p, size_t e, const Strides& x) { return at(p, 4 * e) && x.b % 4 == 0 && x.t % 4 == 0; }
+bool wide_ok(const void* p, size_t e, const Strides& x) {
+  const long long v = 16 / e;
+  return at(p, 16) && x.b % v == 0 && x.t % v == 0;
+}
 
 arl2_status check(const arl2_scan_shape& s, bool* head) {
   if (s.B < 1 || s.T < 1 || s.C < 1 || s.heads < 0) return ARL2_ERR_INVALID_ARG;
@@ -602,9 +776,9 @@ arl2_status current_device(int* dev) {
 }
 
 size_t workspace_bytes(const arl2_scan_shape& s) {
-  // Whether groups of 4 channels can be accessed at once is known only with the pointers.
+  // Whether 16 bytes can be accessed at once is known only with the pointers.
   size_t pairs = 0;
-  for (int V : {1, 4}) {
+  for (int V : {1, static_cast<int>(16 / elem(s.dtype))}) {
     const ScanPlan p = plan_scan(s.B, s.T, s.C, V);
     pairs = std::max(pairs, p.slice_pairs + p.chunk_pairs);
   }
@@ -636,7 +810,7 @@ extern "C" arl2_status arl2_scan_forward(const arl2_scan_fwd* f, arl2_stream str
   if (!strides_ok(xs, s.B, s.T, s.C, false) || !strides_ok(as, s.B, s.T, s.C, false) ||
       !strides_ok(hs, s.B, s.T, s.C, true))
     return ARL2_ERR_INVALID_ARG;
-  bool wide = s.C % 4 == 0 && wide_ok(f->x, e, xs) && wide_ok(f->h, e, hs);
+  bool wide = s.C % (16 / e) == 0 && wide_ok(f->x, e, xs) && wide_ok(f->h, e, hs);
   if (head && !wide) return ARL2_ERR_INVALID_ARG;
   if (!head) wide = wide && wide_ok(f->a, ge, as);
   if (needs_workspace(s) && !(f->workspace && at(f->workspace, 16))) return ARL2_ERR_INVALID_ARG;
@@ -676,9 +850,9 @@ extern "C" arl2_status arl2_scan_backward(const arl2_scan_bwd* f, arl2_stream st
   if (!strides_ok(gs, s.B, s.T, s.C, false) || !strides_ok(hs, s.B, s.T, s.C, false) ||
       !strides_ok(as, s.B, s.T, s.C, false) || !strides_ok(xs, s.B, s.T, s.C, true))
     return ARL2_ERR_INVALID_ARG;
-  bool wide = s.C % 4 == 0 && wide_ok(f->dh, e, gs) && wide_ok(f->h, e, hs) && wide_ok(f->dx, e, xs);
+  bool wide = s.C % (16 / e) == 0 && wide_ok(f->dh, e, gs) && wide_ok(f->h, e, hs) && wide_ok(f->dx, e, xs);
   if (head && !wide) return ARL2_ERR_INVALID_ARG;
-  if (!head) wide = wide && wide_ok(f->a, ge, as) && at(f->da, 4 * ge);
+  if (!head) wide = wide && wide_ok(f->a, ge, as) && at(f->da, 16);
   if (needs_workspace(s) && !(f->workspace && at(f->workspace, 16))) return ARL2_ERR_INVALID_ARG;
   int dev = 0;
   const arl2_status ds = current_device(&dev);
