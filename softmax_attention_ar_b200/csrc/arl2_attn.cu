@@ -16,7 +16,7 @@ struct arl2_attn {
   float* records = nullptr;        // partial records of shared tiles, two per CTA
   float* dq_records = nullptr;     // the dq kernel's
   float* stats = nullptr;          // backward: row statistics
-  unsigned int* err = nullptr;
+  unsigned int* err = nullptr;     // the error word, then the backward kernel's two tickets
   unsigned long long timeout_ns = 1000000000ull;
   size_t bytes = 0;
 };
@@ -97,8 +97,9 @@ bool shares_tiles(const arl2_attn* c, const arl2_attn_shape* s, bool forward) {
   if (s->q_len || s->k_len || s->frame_len) return true;
   const long long qt = tiles(s->Tq, 128), kt = tiles(s->Tk, 128), bh = static_cast<long long>(c->B) * c->H;
   if (forward) return cuts_tiles(bh * tiles(s->Tq, 256), kt, c->sms);
-  return cuts_tiles(bh * qt, kt, c->sms) ||
-         cuts_tiles(static_cast<long long>(c->B) * c->Hkv * kt, qt * (c->H / c->Hkv), c->sms);
+  const int n_dkv = arl2::attn_dkv_ctas(c->sms);
+  return cuts_tiles(bh * qt, kt, c->sms - n_dkv) ||
+         cuts_tiles(static_cast<long long>(c->B) * c->Hkv * kt, qt * (c->H / c->Hkv), n_dkv);
 }
 
 arl2::AttnOut out_of(const arl2_tensor* t) {
@@ -116,6 +117,7 @@ arl2::AttnArgs args_of(const arl2_attn* c, const arl2_attn_shape* s) {
   a.records = c->records;
   a.dq_records = c->dq_records;
   a.err = c->err;
+  a.tickets = c->err + 1;
   a.timeout_ns = c->timeout_ns;
   return a;
 }
@@ -154,7 +156,7 @@ arl2_status arl2_attn_create(int B, int H, int H_kv, int max_Tq, int max_Tk, int
   const size_t bh = static_cast<size_t>(B) * H;
   const bool ok = alloc(&c->records, 2 * static_cast<size_t>(sms) * arl2::attn_record_floats(d), &c->bytes) &&
                   alloc(&c->dq_records, 2 * static_cast<size_t>(sms) * arl2::attn_dq_record_floats(d), &c->bytes) &&
-                  alloc(&c->stats, bh * 2 * tiles(max_Tq, 128) * 128, &c->bytes) && alloc(&c->err, 1, &c->bytes) &&
+                  alloc(&c->stats, bh * 2 * tiles(max_Tq, 128) * 128, &c->bytes) && alloc(&c->err, 3, &c->bytes) &&
                   cudaMemset(c->err, 0, sizeof(unsigned int)) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     arl2_attn_destroy(c);
@@ -213,6 +215,7 @@ arl2_status arl2_attn_backward(arl2_attn* c, const arl2_attn_bwd* f, arl2_stream
   p.lse = f->lse;
   p.stats = c->stats;
   p.q_len = s->q_len;
+  p.tickets = c->err + 1;
   p.B = c->B, p.H = c->H, p.Tq = s->Tq, p.d = c->d;
   arl2::AttnArgs a = args_of(c, s);
   a.o = out_of(&f->dq);

@@ -7,9 +7,10 @@
 // The tensor cores bound it. Launches, each a programmatic dependent of the one before:
 //   - arl2_attn_prep_kernel: -delta, and -lse in log2 units (-inf where a row sees nothing or lies
 //     behind its length: P is then 0 or next to it), padded to whole 128-row tiles;
-//   - arl2_attn_dkv_kernel: a tile is 128 keys of one key head; it runs over the query tiles of
-//     every query head that shares the head, so the heads' sum stays in the accumulators;
-//   - arl2_attn_dq_kernel: a tile is 128 query rows of one head; it runs over the key tiles;
+//   - arl2_attn_bwd_kernel, some of whose CTAs compute dk and dv (dkv_cta): a tile is 128 keys of
+//     one key head and runs over the query tiles of every query head that shares the head, so the
+//     heads' sum stays in the accumulators; and the others dq (dq_cta): a tile is 128 query rows of
+//     one head and runs over the key tiles;
 //   - arl2_attn_bwd_combine_kernel: adds up the records of tiles shared between CTAs.
 // S and dP are computed in both, 7 products a tile pair instead of the 5 of a single pass. In
 // return no dq leaves the SM before it is complete: a single pass would add 64 KiB of fp32 per
@@ -103,6 +104,7 @@ __device__ __forceinline__ void add_records(Rec&& record, int c0, int c1, int q0
 template <bool kHalf>
 __global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_constant__ AttnPrepArgs a) {
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.tickets[threadIdx.x] = 0;
   const int lanes = a.d / 8;                        // lanes per row, 16 bytes each
   const int Tpad = (a.Tq + kRows - 1) / kRows * kRows;
   const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / lanes;   // (b, t, h), h fastest
@@ -166,12 +168,10 @@ enum : int {
 static_assert(kKBars * 8 <= 320, "control block");
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    arl2_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
-                         const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                        const CUtensorMap& tm_g, const AttnArgs& a, uint8_t* attn_smem, int cta,
+                                        int nctas) {
   using TO = TileOf<D>;
-  extern __shared__ __align__(1024) uint8_t attn_smem[];
   const uint32_t base = smem_u32(attn_smem);
   const uint32_t k_tile = base, v_tile = base + TO::kBytes, q_ring = base + 2 * TO::kBytes,
                  g_ring = base + 5 * TO::kBytes, t_ring = base + 7 * TO::kBytes, ctl = t_ring + 2048;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       prefetch_tmap(&tm_g);
     }
     __syncwarp();
-    make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, blockIdx.x, gridDim.x, &shared->split);
+    make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, cta, nctas, &shared->split);
   }
   if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
   tc_fence_before();
@@ -241,7 +241,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         if (!waited) {   // the statistics come from the launch before this one
           griddep_wait();
-          griddep_launch_dependents();
           waited = true;
         }
         if (lead) {
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       ++ns;
       tc_fence_after();
-      float* rec = a.records + record_slot(sp, blockIdx.x, sg.first) * attn_record_floats(D) + wg * D * kRows;
+      float* rec = a.records + record_slot(sp, cta, sg.first) * attn_record_floats(D) + wg * D * kRows;
       write_rows<D, kHalf>(sg, (wg ? c_dk : c_dv) + lanes, r, inside, j >= sg.kl, dst, wg ? a.scale : 1.f, rec,
                            bar(kKAccEmpty));
     }
@@ -483,12 +482,10 @@ static_assert(kQBars * 8 <= 320, "control block");
 using QTiles = RowTiles<kRows>;
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    arl2_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
-                        const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                       const CUtensorMap& tm_g, const AttnArgs& a, uint8_t* attn_smem, int cta,
+                                       int nctas) {
   using TO = TileOf<D>;
-  extern __shared__ __align__(1024) uint8_t attn_smem[];
   const uint32_t base = smem_u32(attn_smem);
   const uint32_t q_tile = base, g_tile = base + TO::kBytes, k_ring = base + 2 * TO::kBytes,
                  v_ring = base + 5 * TO::kBytes, ctl = base + 7 * TO::kBytes;
@@ -499,7 +496,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Guard g{&shared->abort, a.err, a.timeout_ns};
   const int group = a.H / a.Hkv;
 
-  griddep_launch_dependents();   // the combining launch waits for this grid's end before it reads
   if (threadIdx.x == 0) {
     for (int i = 0; i < kQBars; ++i)
       mbar_init(bar(i), i == kQDReady || i == kQAccEmpty ? 8 : i == kQFinal ? 9 : 1);
@@ -514,7 +510,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       prefetch_tmap(&tm_g);
     }
     __syncwarp();
-    make_split<QTiles>(a.mask, a.B, a.H, 1, blockIdx.x, gridDim.x, &shared->split);
+    make_split<QTiles>(a.mask, a.B, a.H, 1, cta, nctas, &shared->split);
   }
   if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
   tc_fence_before();
@@ -557,7 +553,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     __syncwarp();
-    griddep_wait();   // this grid ends after the one before it
     // Every copy issued lands before the CTA may exit.
     if (ns > 0) mbar_wait_drain(bar(kQQFull), (ns - 1) & 1);
     for (uint32_t s = 0; s < 3; ++s)
@@ -645,6 +640,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool writes = D > 32 || wg == 0;
     uint32_t n = 0, ns = 0;
     bool ok = true;
+    griddep_wait();   // the statistics come from the launch before this one
     while (ok && walk.next(sg)) {
       const int row = sg.tile * kRows + r;
       uint16_t* dst = a.o.ptr + sg.b * a.o.sb + row * a.o.st + sg.h * a.o.sh + kCols * wg;
@@ -703,7 +699,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       ++ns;
       tc_fence_after();
-      float* rec = a.dq_records + record_slot(sp, blockIdx.x, sg.first) * attn_dq_record_floats(D) + wg * kCols * kRows;
+      float* rec = a.dq_records + record_slot(sp, cta, sg.first) * attn_dq_record_floats(D) + wg * kCols * kRows;
       if (writes)
         write_rows<kCols, kHalf>(sg, c_dq + lanes + kCols * wg, r, inside, row >= sg.ql, dst, a.scale, rec,
                                  bar(kQAccEmpty));
@@ -723,21 +719,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ one launch of both
+// n_dkv CTAs compute dk and dv, the others dq: one start-up, one end and half as many shared tiles
+// as two launches that each use every SM. Where the two SMs of a pair (2 i, 2 i + 1) run different
+// kinds, both run up to 1.4 times as long (measured; the cause is not known). So a CTA asks for its work by the SM it finds itself
+// on, and gets the next range of that kind, or of the other one once it has run out. Which CTA
+// computes a range changes nothing in the result.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    arl2_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                         const __grid_constant__ AttnArgs a, int n_dkv) {
+  extern __shared__ __align__(1024) uint8_t attn_smem[];
+  griddep_launch_dependents();   // the combining launch waits for this grid's end before it reads
+  const int n_dq = static_cast<int>(gridDim.x) - n_dkv;
+  int* ticket = reinterpret_cast<int*>(attn_smem);
+  if (threadIdx.x == 0) {
+    griddep_wait();   // the launch before this one zeroed the tickets
+    uint32_t sm;
+    asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
+    int kind = static_cast<int>(sm & ~1u) < n_dkv ? 0 : 1;
+    int c = static_cast<int>(atomicAdd(a.tickets + kind, 1u));
+    if (c >= (kind ? n_dq : n_dkv)) {
+      kind ^= 1;
+      c = static_cast<int>(atomicAdd(a.tickets + kind, 1u));
+    }
+    ticket[0] = kind;
+    ticket[1] = c;
+  }
+  __syncthreads();
+  const int kind = ticket[0], c = ticket[1];
+  __syncthreads();   // read before the CTA lays out its shared memory
+  if (kind == 0)
+    dkv_cta<D, kHalf>(tm_q, tm_k, tm_v, tm_g, a, attn_smem, c, n_dkv);
+  else
+    dq_cta<D, kHalf>(tm_q, tm_k, tm_v, tm_g, a, attn_smem, c, n_dq);
+}
+
 // ------------------------------------------------------------------ records
 // Adds up the records of the tiles shared between CTAs, as the forward's (arl2_attn_fwd.cu): block
 // (c, y) takes 32 columns of the tile at the start of CTA c's range; y < D / 32: of dv, then of
 // dk, then, in the dq kernel's split, of dq.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const __grid_constant__ AttnArgs a, int n_dkv, int n_dq) {
   __shared__ Split split;
   constexpr int kParts = D / 32;
   const int c = static_cast<int>(blockIdx.x) + 1, r = threadIdx.x, what = blockIdx.y / kParts;
   const int k0 = 32 * (blockIdx.y % kParts), group = a.H / a.Hkv;
   if (threadIdx.x < 32) {
     if (what < 2)
-      make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, c, gridDim.x + 1, &split);
+      make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, c, n_dkv, &split);
     else
-      make_split<QTiles>(a.mask, a.B, a.H, 1, c, gridDim.x + 1, &split);
+      make_split<QTiles>(a.mask, a.B, a.H, 1, c, n_dq, &split);
   }
   __syncthreads();
   const Split sp = split;
@@ -766,10 +799,7 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const _
 
 template <int D, bool kHalf>
 cudaError_t setup() {
-  cudaError_t e = cudaFuncSetAttribute(arl2_attn_dkv_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(bwd_smem<D>()));
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(arl2_attn_dq_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(arl2_attn_bwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(bwd_smem<D>()));
 }
 template <int D, bool kHalf>
@@ -778,12 +808,13 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   const long long rows = static_cast<long long>(a.B) * ((a.mask.Tq + kRows - 1) / kRows * kRows) * a.H;
   const unsigned blocks = static_cast<unsigned>((rows * (D / 8) + 255) / 256);
   cudaError_t e = launch_chained(arl2_attn_prep_kernel<kHalf>, dim3(blocks), 256, 0, st, false, prep);
+  const int n_dkv = attn_dkv_ctas(ctas), n_dq = ctas - n_dkv;
   if (e == cudaSuccess)
-    e = launch_chained(arl2_attn_dkv_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a);
-  if (e == cudaSuccess)
-    e = launch_chained(arl2_attn_dq_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a);
-  if (e != cudaSuccess || !combine || ctas < 2) return e;
-  return launch_chained(arl2_attn_bwd_combine_kernel<D, kHalf>, dim3(ctas - 1, 3 * (D / 32)), kRows, 0, st, true, a);
+    e = launch_chained(arl2_attn_bwd_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a,
+                       n_dkv);
+  if (e != cudaSuccess || !combine) return e;
+  return launch_chained(arl2_attn_bwd_combine_kernel<D, kHalf>, dim3(std::max(n_dkv, n_dq), 3 * (D / 32)), kRows, 0, st,
+                        true, a, n_dkv, n_dq);
 }
 
 }  // namespace

@@ -25,6 +25,7 @@ struct AttnArgs {
   const float* stats;     // backward: [B H][2][Tq rounded up to 128]: -lse in log2 units, then -delta
   float* records;         // partial records, two per CTA
   float* dq_records;      // the dq kernel's
+  unsigned int* tickets;  // backward: ranges handed out, [dk and dv, dq]
   unsigned int* err;
   unsigned long long timeout_ns;
 };
@@ -37,6 +38,7 @@ struct AttnPrepArgs {
   const float* lse;       // [B, H, Tq]
   float* stats;
   const int* q_len;
+  unsigned int* tickets;  // zeroed
   int B, H, Tq, d;
 };
 
@@ -44,6 +46,10 @@ __host__ __device__ constexpr size_t attn_record_floats(int d) { return 2ull * 1
 __host__ __device__ constexpr size_t attn_dq_record_floats(int d) { return 128ull * d; }
 cudaError_t attn_fwd_setup();
 cudaError_t attn_bwd_setup();
+// Of the backward kernel's CTAs, those that compute dk and dv; the others compute dq. Both have the
+// same tile pairs to do, of 4 and 3 products: 2590 and 2230 cycles each as measured at d = 128.
+// An even number, for whole pairs of SMs.
+inline int attn_dkv_ctas(int ctas) { return ctas < 4 ? 1 : (ctas * 259 / (259 + 223) + 1) / 2 * 2; }
 // Each launches as a programmatic dependent of the one before it in the same call. combine: a
 // tile may be shared between CTAs, so its records have to be added up.
 cudaError_t launch_attn_fwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
