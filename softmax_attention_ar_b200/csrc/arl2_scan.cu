@@ -15,17 +15,20 @@
 //     every chunk to the workspace;
 //   - arl2_scan_apply_kernel composes the pairs before each slice onto the initial state,
 //     then streams the slice again from that state and writes the results.
-// The second reading is what this costs over a single pass. It comes from L2 as far as x and a fit
-// there: the first launch goes through each slice from its end to its start, so that the second
-// begins with what was read last, and results are stored evict-first. A single-pass form (a cluster's CTAs following one another in time, pairs
-// exchanged through distributed shared memory, data kept in a ring) reads everything once but
-// moves in lock step with a barrier per 1024 tokens: it measured 115 us on 32760 tokens of
-// 1536 bf16 channels. A sequence that one chunk holds takes one launch, without workspace.
+// The second reading is what this costs over a single pass: 100 + 100 read and 100 written MB take
+// 58 us on 32760 tokens of 1536 bf16 channels (5.2 TB/s; without the stores 43 us). Part of it comes
+// from L2: the first launch goes through each slice from its end to its start, so that the second
+// begins with what was read last, and results are stored evict-first. Cutting long sequences into
+// segments that fit L2, one launch each, lost more to the launches (81 us). A single-pass form (a
+// cluster's CTAs following one another in time, pairs exchanged through distributed shared memory)
+// moved in lock step with a barrier per 1024 tokens (115 us). A sequence that one chunk holds takes
+// one launch, without workspace.
 // The order of all products and sums is fixed, so results do not depend on timing. All of it is
 // fp32; only the stored h, dx and da are rounded, once, to their types.
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -72,19 +75,54 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
+// Two 16-bit values, and two fp32 ones rounded to them.
+template <typename T>
+__device__ __forceinline__ float2 widen_pair(uint32_t w) {
+  if constexpr (std::is_same_v<T, __half>)
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
+}
+
 // V values of type T, accessed 16 bytes at a time.
 template <typename T, int V>
 struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
   T v[V];
   __device__ __forceinline__ void widen(float (&f)[V]) const {
+    if constexpr (sizeof(T) == 2 && V > 1) {   // by pairs: one instruction a value
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_f(v[i]);
+      for (int i = 0; i < V; i += 2) {
+        const float2 x = widen_pair<T>(w[i / 2]);
+        f[i] = x.x;
+        f[i + 1] = x.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = to_f(v[i]);
+    }
   }
   __device__ __forceinline__ void round(const float (&f)[V]) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = from_f<T>(f[i]);
+      for (int i = 0; i < V; i += 2) w[i / 2] = round_pair<T>(f[i], f[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = from_f<T>(f[i]);
+    }
   }
 };
+
 // A load that stays where it is written: the compiler would otherwise move each next to its use, to
 // save registers, and the loads of a batch would wait for one another.
 template <typename P>
@@ -579,7 +617,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         } else {
           PG o2;
 #pragma unroll
-          for (int v = 0; v < GV; ++v) o2.v[v] = from_f<G>(state[v] * hf[v]);
+          for (int v = 0; v < GV; ++v) hf[v] *= state[v];
+          o2.round(hf);
           if (ok) store_streaming(pa, o2);
           pa -= a.da_t;
         }
@@ -620,11 +659,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
   }
 }
 
-// How a call is cut. The CTAs are to fill the GPU once, two for each SM of a B200: more would mean more pairs
-// to write and to compose (each CTA composes all the chunks before its own), fewer leave SMs
-// idle (without the ring, twice as many: their loads are hidden by other warps alone). So chunks are as many as that allows, at most 256 a sequence, in slices of 8 tokens or
-// more. A sequence of at most one chunk of 64-token slices is one chunk, cut into no more parts
-// than it has batches.
+// How a call is cut. The CTAs are to fill the GPU once, two for each SM of a B200: more would mean
+// more pairs to write and to compose (each CTA composes all the chunks before its own), fewer leave
+// SMs idle (32760 tokens of 1536 channels: 62 us with two, 72 with three, 79 with four). Without the
+// ring, twice as many: their loads are hidden by other warps alone. So chunks are as many as that
+// allows, at most 256 a sequence, in slices of 8 tokens or more. A sequence of at most one chunk of
+// 64-token slices is one chunk, cut into no more parts than it has batches.
 struct ScanPlan {
   int lanes, groups, slice, nchunks, warps;
   size_t slice_pairs, chunk_pairs;   // workspace, in (A, X) pairs
