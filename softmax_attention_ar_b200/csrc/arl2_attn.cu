@@ -87,8 +87,9 @@ bool tensor_map(CUtensorMap* m, const arl2_tensor* t, int B, int T, int heads, i
 
 // Whether the split may give parts of a tile to several CTAs. Without lengths and frames every tile
 // has the same units, and the ranges' starts tell; otherwise only the device knows.
-bool cuts_tiles(long long ntiles, long long units, int grid) {
+bool cuts_tiles(long long ntiles, long long units, int grid, int cut_cost) {
   const long long total = ntiles * units, ctas = arl2::split_ctas(ntiles, total, grid);
+  if (arl2::split_whole(ntiles, total, units, grid, cut_cost)) return false;
   for (long long i = 1; i < ctas; ++i)
     if (i * total / ctas % units != 0) return true;
   return false;
@@ -96,10 +97,11 @@ bool cuts_tiles(long long ntiles, long long units, int grid) {
 bool shares_tiles(const arl2_attn* c, const arl2_attn_shape* s, bool forward) {
   if (s->q_len || s->k_len || s->frame_len) return true;
   const long long qt = tiles(s->Tq, 128), kt = tiles(s->Tk, 128), bh = static_cast<long long>(c->B) * c->H;
-  if (forward) return cuts_tiles(bh * tiles(s->Tq, 256), kt, c->sms);
+  if (forward) return cuts_tiles(bh * tiles(s->Tq, 256), kt, c->sms, arl2::RowTiles<256>::kCutCost);
   const int n_dkv = arl2::attn_dkv_ctas(c->sms);
-  return cuts_tiles(bh * qt, kt, c->sms - n_dkv) ||
-         cuts_tiles(static_cast<long long>(c->B) * c->Hkv * kt, qt * (c->H / c->Hkv), n_dkv);
+  return cuts_tiles(bh * qt, kt, c->sms - n_dkv, arl2::RowTiles<128>::kCutCost) ||
+         cuts_tiles(static_cast<long long>(c->B) * c->Hkv * kt, qt * (c->H / c->Hkv), n_dkv,
+                    arl2::KeyTiles::kCutCost);
 }
 
 arl2::AttnOut out_of(const arl2_tensor* t) {

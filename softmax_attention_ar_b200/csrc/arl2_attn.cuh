@@ -11,7 +11,8 @@
 // The units of all tiles, in order, are cut into equal contiguous ranges, one per CTA, so that
 // every SM gets the same work whatever the lengths and masks are. A tile whose units fall to
 // several CTAs is a sum of partial records in the workspace: a launch that follows adds them in
-// the order of the CTAs, so the result does not depend on timing. No CTA waits for another.
+// the order of the CTAs, so the result does not depend on timing. No CTA waits for another. Where
+// whole tiles, one per CTA, take hardly longer than equal ranges would, nothing is cut.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -56,6 +57,10 @@ __device__ __forceinline__ int first_row(const AttnMask& m, int j) {
 // query tile) pairs that see its first key.
 template <int kRowsPerTile>
 struct RowTiles {
+  // What cutting tiles costs, in units per CTA: records to write, the pipeline to fill again, and
+  // the launch that adds. Forward, one 480p frame of 12 heads: 84 tiles of 13 units take 37 us
+  // whole and 43 us cut into 148 ranges of 7.4 units. Backward, it hardly matters.
+  static constexpr int kCutCost = kRowsPerTile == kRows ? 2 : 8;
   static __device__ int count(const AttnMask& m) { return (m.Tq + kRowsPerTile - 1) / kRowsPerTile; }
   static __device__ int valid(const AttnMask& m, int ql, int) { return (ql + kRowsPerTile - 1) / kRowsPerTile; }
   static __device__ int units(const AttnMask& m, int i, int ql, int kl, int) {
@@ -64,6 +69,7 @@ struct RowTiles {
   }
 };
 struct KeyTiles {
+  static constexpr int kCutCost = 2;
   static __device__ int count(const AttnMask& m) { return (m.Tk + kRows - 1) / kRows; }
   static __device__ int valid(const AttnMask& m, int, int kl) { return (kl + kRows - 1) / kRows; }
   static __device__ int first_tile(const AttnMask& m, int j) { return max(0, first_row(m, j * kRows)) / kRows; }
@@ -83,26 +89,39 @@ struct Split {
   long long u0, u1, total;
   int ctas;                  // CTAs that have a range
   int b, h, tile, off;       // of unit u0
+  int whole;                 // nothing is cut: CTA c has tile c, and its first unit is u0 = 0
 };
 
-// Sum over a batch's tiles of the units of one head (at least one each), by one warp.
+// Sum over a batch's tiles of the units of one head (at least one each), and the most that a tile
+// has, by one warp.
 template <typename Tiles>
-__device__ long long head_units(const AttnMask& m, int b, int group) {
+__device__ long long head_units(const AttnMask& m, int b, int group, int* most) {
   const int ql = q_length(m, b), kl = k_length(m, b), n = Tiles::count(m);
   if (m.F == 0) {   // every valid tile has the same
-    const int v = Tiles::valid(m, ql, kl);
-    return static_cast<long long>(v) * max(1, Tiles::units(m, 0, ql, kl, group)) + (n - v);
+    const int v = Tiles::valid(m, ql, kl), u = max(1, Tiles::units(m, 0, ql, kl, group));
+    *most = max(*most, u);
+    return static_cast<long long>(v) * u + (n - v);
   }
   long long s = 0;
-  for (int i = threadIdx.x & 31; i < n; i += 32) s += max(1, Tiles::units(m, i, ql, kl, group));
+  int top = 1;
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    const int u = max(1, Tiles::units(m, i, ql, kl, group));
+    s += u;
+    top = max(top, u);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  *most = max(*most, __reduce_max_sync(0xffffffffu, top));
   return s;
 }
 
-// The number of CTAs that get a range. Few units per CTA cost more in adding up records than they
+// Whether nothing is cut, and the number of CTAs that get a range otherwise. Few units per CTA cost more in adding up records than they
 // save: at least kMinUnits each, unless the tiles alone are more.
 constexpr int kMinUnits = 4;
+__host__ __device__ inline bool split_whole(long long tiles, long long total, long long most, long long grid,
+                                            int cut_cost) {
+  return tiles <= grid && most * grid <= total + cut_cost * grid;
+}
 __host__ __device__ inline long long split_ctas(long long tiles, long long total, long long grid) {
   long long n = total / kMinUnits;
   n = n > tiles ? n : tiles;
@@ -115,17 +134,32 @@ template <typename Tiles>
 __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c, int grid, Split* out) {
   const int lane = threadIdx.x & 31;
   const bool ragged = m.q_len || m.k_len;
+  const int n = Tiles::count(m);
   long long total = 0, per_head = 0;
+  int most = 1;
   if (!ragged) {
-    per_head = head_units<Tiles>(m, 0, group);
+    per_head = head_units<Tiles>(m, 0, group, &most);
     total = per_head * heads * B;
   } else {
-    for (int b = 0; b < B; ++b) total += head_units<Tiles>(m, b, group) * heads;
+    for (int b = 0; b < B; ++b) total += head_units<Tiles>(m, b, group, &most) * heads;
   }
-  const long long ctas = split_ctas(static_cast<long long>(Tiles::count(m)) * heads * B, total, grid);
+  const long long tiles = static_cast<long long>(n) * heads * B;
   Split s{};
-  s.ctas = static_cast<int>(ctas);
   s.total = total;
+  if (split_whole(tiles, total, most, grid, Tiles::kCutCost)) {
+    s.whole = 1;
+    s.ctas = static_cast<int>(tiles);
+    if (c < s.ctas) {
+      s.b = c / (heads * n);
+      s.h = c / n % heads;
+      s.tile = c % n;
+      s.u1 = max(1, Tiles::units(m, s.tile, q_length(m, s.b), k_length(m, s.b), group));
+    }
+    if (lane == 0) *out = s;
+    return;
+  }
+  const long long ctas = split_ctas(tiles, total, grid);
+  s.ctas = static_cast<int>(ctas);
   if (c < ctas) {
     s.u0 = quick_div(c * total, ctas);
     s.u1 = quick_div((c + 1) * total, ctas);
@@ -136,14 +170,14 @@ __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c
       r -= s.b * per_batch;
     } else {
       for (; s.b < B; ++s.b) {
-        per_head = head_units<Tiles>(m, s.b, group);
+        per_head = head_units<Tiles>(m, s.b, group, &most);
         if (r < per_head * heads) break;
         r -= per_head * heads;
       }
     }
     s.h = static_cast<int>(quick_div(r, per_head));
     r -= s.h * per_head;
-    const int ql = q_length(m, s.b), kl = k_length(m, s.b), n = Tiles::count(m);
+    const int ql = q_length(m, s.b), kl = k_length(m, s.b);
     if (m.F == 0) {
       const int v = Tiles::valid(m, ql, kl), w = max(1, Tiles::units(m, 0, ql, kl, group));
       if (r < static_cast<long long>(v) * w) {

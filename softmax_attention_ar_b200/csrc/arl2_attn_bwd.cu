@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const _
   const Split sp = split;
   griddep_wait();   // the records; every block, so that this grid ends after the one before it
   const long long first = sp.u0 - sp.off;
-  if (c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
+  if (sp.whole || c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
   const int ql = q_length(a.mask, sp.b), kl = k_length(a.mask, sp.b);
   const int units = what < 2 ? KeyTiles::units(a.mask, sp.tile, ql, kl, group) : QTiles::units(a.mask, sp.tile, ql, kl, 1);
   const int c1 = unit_owner(sp, first + max(1, units) - 1);

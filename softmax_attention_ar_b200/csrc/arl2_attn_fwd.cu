@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const _
   const Split sp = split;
   griddep_wait();   // the records; every block, so that this grid ends after the one before it
   const long long first = sp.u0 - sp.off;
-  if (c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
+  if (sp.whole || c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
   const int i = blockIdx.y & 1, k0 = 32 * (blockIdx.y >> 1);
   const int ql = q_length(a.mask, sp.b), kl = k_length(a.mask, sp.b);
   const int row = sp.tile * kFwdRows + i * kRows + r;
