@@ -140,21 +140,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           load_tile<D>(q_tile + i * TO::kBytes, &tm_q, bar(kFQFull), sg.h, sg.tile * kFwdRows + i * kRows, sg.b);
       }
       ++ns;
-      for (int t = sg.kb; ok && t < sg.ke; ++t) {
-        for (int kv = 0; kv < 2; ++kv, ++r) {
-          const uint32_t st = r % kRing;
-          if (r >= kRing && !mbar_wait_warp(bar(kFEmpty + st), (r / kRing - 1) & 1, g)) {
-            ok = false;
-            break;
-          }
-          // Values behind the length must not reach P V; keys there are masked in the scores.
-          const int r0 = kv == 1 && sg.kl < a.mask.Tk ? sg.kl - t * kRows : kRows;
-          if (!load_clean<D>(ring0 + st * TO::kBytes, kv ? &tm_v : &tm_k, bar(kFFull + st), bar(kFSide), side_phase,
-                             sg.h / group, t * kRows, sg.b, r0, lead, g)) {
-            ++r;
-            ok = false;
-            break;
-          }
+      const int n = sg.ke - sg.kb;
+      for (int k = 0; k < 2 * n; ++k, ++r) {
+        // K and V by turns; in a narrow tile the keys run one tile ahead.
+        const int kv = tiles == 2 ? k & 1 : k < 2 ? n == 1 && k == 1 : k == 2 * n - 1 || !(k & 1);
+        const int t = sg.kb + (tiles == 2 ? k >> 1 : kv ? (k == 2 * n - 1 ? n - 1 : k / 2 - 1) : k < 2 ? k : (k + 1) / 2);
+        const uint32_t st = r % kRing;
+        ok = r < kRing || mbar_wait_warp(bar(kFEmpty + st), (r / kRing - 1) & 1, g);
+        if (!ok) break;
+        // Values behind the length must not reach P V; keys there are masked in the scores.
+        const int r0 = kv && sg.kl < a.mask.Tk ? sg.kl - t * kRows : kRows;
+        ok = load_clean<D>(ring0 + st * TO::kBytes, kv ? &tm_v : &tm_k, bar(kFFull + st), bar(kFSide), side_phase,
+                           sg.h / group, t * kRows, sg.b, r0, lead, g);
+        if (!ok) {
+          ++r;
+          break;
         }
       }
     }
@@ -185,41 +185,44 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tc_fence_after();
       if (tiles == 1) {
         // Narrow: the two groups take the key tiles by turns, each with an S and an O of its own.
-        for (int t = 0; ok && t < min(n, 2); ++t) {
-          ok = full(r + 2 * t);
-          if (!ok) break;
+        // Ring order K0 K1 V0 K2 V1 .. (as the copying warp's).
+        auto at_k = [&](int t) { return r + (t < 2 ? t : 2 * t - 1); };
+        auto at_v = [&](int t) { return r + (t < n - 1 ? 2 * t + 2 : 2 * n - 1); };
+        auto scores = [&](int t) {
+          const uint32_t p = at_k(t);
+          if (!full(p)) return false;
           tc_fence_after();
           if (lead) {
-            mma_over_d<D>(tmem + 128u * t, q_tile, slot(r + 2 * t), id_s);
-            mma_commit(bar(kFSFull + t));
-            mma_commit(bar(kFEmpty + (r + 2 * t) % kRing));
+            mma_over_d<D>(tmem + 128u * (t & 1), q_tile, slot(p), id_s);
+            mma_commit(bar(kFSFull + (t & 1)));
+            mma_commit(bar(kFEmpty + p % kRing));
           }
           __syncwarp();
-        }
-        for (int t = 0; ok && t < n; ++t, r += 2) {
+          return true;
+        };
+        ok = scores(0) && (n < 2 || scores(1));
+        for (int t = 0; ok && t < n; ++t) {
           const int i = t & 1;
-          ok = full(r + 1) && (t + 2 >= n || full(r + 4));
+          const uint32_t p = at_v(t);
+          ok = full(p);
           if (ok && t < 2 && nseg[i] > 0) ok = mbar_wait_warp(bar(kFOEmpty + i), (nseg[i] - 1) & 1, g);
           ok = ok && mbar_wait_warp(bar(kFPReady + 2 * i), np[i] & 1, g);
           if (!ok) break;
           tc_fence_after();
-          if (lead) mma_over_half_rows<0>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, t > 1);
+          if (lead) mma_over_half_rows<0>(tmem + 256u + 128u * i, tmem + 128u * i, slot(p), id_o, t > 1);
           __syncwarp();
           ok = mbar_wait_warp(bar(kFPReady + 2 * i + 1), np[i] & 1, g);
           if (!ok) break;
           ++np[i];
           tc_fence_after();
           if (lead) {
-            mma_over_half_rows<1>(tmem + 256u + 128u * i, tmem + 128u * i, slot(r + 1), id_o, 1u);
-            mma_commit(bar(kFEmpty + (r + 1) % kRing));
-            if (t + 2 < n) {
-              mma_over_d<D>(tmem + 128u * i, q_tile, slot(r + 4), id_s);
-              mma_commit(bar(kFSFull + i));
-              mma_commit(bar(kFEmpty + (r + 4) % kRing));
-            }
+            mma_over_half_rows<1>(tmem + 256u + 128u * i, tmem + 128u * i, slot(p), id_o, 1u);
+            mma_commit(bar(kFEmpty + p % kRing));
           }
           __syncwarp();
+          ok = t + 2 >= n || scores(t + 2);
         }
+        r += 2 * n;
         if (!ok) break;
         if (lead) {
           mma_commit(bar(kFOFull));
