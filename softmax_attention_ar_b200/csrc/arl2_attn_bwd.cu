@@ -653,7 +653,9 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMa
       }
       const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + sg.h) * 2 * Tpad + row;
       const float2 neg_lse = make_float2(st[0], st[0]), neg_delta = make_float2(st[Tpad], st[Tpad]);
-      const int limit = row < sg.ql ? key_limit(a.mask, row, sg.kl) : 0;
+      // Rows behind the length are not written; they count as seeing all, so that they do not make
+      // every tile a masked one.
+      const int limit = row < sg.ql ? key_limit(a.mask, row, sg.kl) : sg.kl;
       for (int t = sg.kb; t < sg.ke; ++t, ++n) {
         ok = mbar_wait_warp(bar(kQSFull + (n & 1)), (n / 2) & 1, g);
         if (!ok) break;

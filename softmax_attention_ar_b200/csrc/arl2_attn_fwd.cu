@@ -315,7 +315,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         row -= i * kRows;   // group 1 helps with the first query tile
       }
       const bool in_q = row < sg.ql;
-      const int limit = in_q ? key_limit(a.mask, row, sg.kl) : 0;
+      // Rows behind the length are not written; they count as seeing all, so that they do not make
+      // every tile a masked one.
+      const int limit = in_q ? key_limit(a.mask, row, sg.kl) : sg.kl;
       // A warp without a row inside the length leaves its P and O as they are: an MMA's rows do not
       // mix, and these are not written.
       const bool idle = row - (r & 31) >= sg.ql;
