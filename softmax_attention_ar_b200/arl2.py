@@ -634,6 +634,7 @@ class SoftmaxAttention:
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
+        self._lse_shapes = {}
         out = _P()
         with torch.cuda.device(self.device):
             _check(self._lib.arl2_attn_create(B, H, self.H_kv, max_Tq, max_Tk, d, DTYPES[dtype], ctypes.byref(out)),
@@ -651,6 +652,16 @@ class SoftmaxAttention:
             self.close()
         except Exception:
             pass
+
+    def _lse_like(self, Tq):
+        """A stand-in (4 bytes) of lse's shape: allocating from one is the quicker call."""
+        t = self._lse_shapes.get(Tq)
+        if t is None:
+            if len(self._lse_shapes) > 64:
+                self._lse_shapes.clear()
+            t = self._lse_shapes[Tq] = torch.empty((1,), dtype=torch.float32, device=self.device).expand(
+                self.B, self.H, Tq)
+        return t
 
     def _lengths(self, q, k):
         for t, name in ((q, "q"), (k, "k")):
@@ -702,11 +713,15 @@ class SoftmaxAttention:
         fields = self._tensor(q, "q", qs) + self._tensor(k, "k", ks) + self._tensor(v, "v", ks)
         if out is None:
             out = torch.empty_like(q)
+            s = out.stride()
+            o = (out.data_ptr(), s[0], s[1], s[2])
+        else:
+            o = self._tensor(out, "out", qs)
         if lse is None:
-            lse = q.new_empty((self.B, self.H, shape[0]), dtype=torch.float32)
+            lse = torch.empty_like(self._lse_like(shape[0]), memory_format=torch.contiguous_format)
         else:
             _want(lse, "lse", self._index, _F32, (self.B, self.H, shape[0]), True)
-        f = _ATTN_FWD.pack(*shape, *fields, *self._tensor(out, "out", qs), lse.data_ptr())
+        f = _ATTN_FWD.pack(*shape, *fields, *o, lse.data_ptr())
         _check(self._lib.arl2_attn_forward(self._c, f, stream), "arl2_attn_forward")
         return out, lse
 
