@@ -384,7 +384,8 @@ void arl2_attn_destroy(arl2_attn* ctx);
  * through workspace: device memory of arl2_scan_workspace_bytes(&shape) bytes (0: none is
  * needed), 16-byte aligned, whose content means nothing before and after a call. Calls that may
  * overlap on the GPU need workspaces of their own. The current device must hold every
- * buffer. */
+ * buffer. The first call of a kind on a device (types, gates, direction) loads its kernel: make it
+ * before any stream capture. */
 typedef struct {
   int B, T, C, heads;
   arl2_dtype dtype, gate_dtype;

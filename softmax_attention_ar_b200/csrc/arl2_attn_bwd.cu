@@ -799,8 +799,13 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const _
     store32<kHalf>(out.ptr + sp.b * out.sb + row * out.st + sp.h * out.sh + k0, y);
 }
 
+// Also loads the kernels, so that a first call inside a stream capture finds them there.
 template <int D, bool kHalf>
 cudaError_t setup() {
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, arl2_attn_prep_kernel<kHalf>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, arl2_attn_bwd_combine_kernel<D, kHalf>);
+  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(arl2_attn_bwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(bwd_smem<D>()));
 }

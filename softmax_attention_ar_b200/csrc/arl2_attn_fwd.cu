@@ -548,8 +548,12 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const _
         sees ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Also loads the kernels, so that a first call inside a stream capture finds them there.
 template <int D, bool kHalf>
 cudaError_t setup() {
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, arl2_attn_fwd_combine_kernel<D, kHalf>);
+  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(arl2_attn_fwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(fwd_smem<D>()));
 }

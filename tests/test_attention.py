@@ -14,7 +14,11 @@ terms whose errors partly cancel):
 fp16 cannot hold values below 2^-14 to e relative: a rounding adds at most 2^-25 per term there.
 """
 import ctypes
+import importlib.util
+import os
+import re
 
+import numpy as np
 import pytest
 import torch
 
@@ -203,6 +207,39 @@ def test_views_of_a_packed_projection():
 
 
 @on_gpu
+def test_offsets_beyond_32_bits():
+    # Every tensor a view whose last token lies 6 GiB behind its first.
+    T, d, step = 4, 32, 1 << 30
+    big = torch.empty((T - 1) * step + 4096, dtype=BF, device="cuda")
+    views = [torch.as_strided(big, (1, T, 1, d), (big.numel(), step, d, 1), 64 * i) for i in range(8)]
+    q, k, v, do = make(1, T, T, 1, 1, d, BF, seed=9)
+    for dst, src in zip(views, (q, k, v, do)):
+        dst.copy_(src)
+    op = arl2.SoftmaxAttention(1, T, T, d)
+    o, lse = op.forward(q, k, v, frame_len=1)
+    want = (o,) + op.backward(do, q, k, v, o, lse, frame_len=1)
+    o2, lse2 = op.forward(*views[:3], out=views[4], frame_len=1)
+    got = (o2,) + op.backward(views[3], *views[:3], o2, lse2, dq=views[5], dk=views[6], dv=views[7], frame_len=1)
+    assert torch.equal(lse, lse2) and all(torch.equal(x, y) for x, y in zip(want, got))
+    assert op.status() == arl2.ARL2_OK
+
+
+@on_gpu
+def test_nan_and_infinity_in_seen_places_stay_in_their_rows():
+    # A NaN key makes the rows that see it NaN and no others; an infinite score as well.
+    for bad in (float("nan"), float("inf")):
+        q, k, v, do = make(1, 300, 300, 2, 2, 64, BF, seed=10)
+        k[0, 200, 0, 0] = bad
+        q[0, :, 0, 0] = q[0, :, 0, 0].abs() + 0.1
+        op = arl2.SoftmaxAttention(2, 300, 300, 64)
+        o, lse = op.forward(q, k, v, frame_len=100)
+        assert op.status() == arl2.ARL2_OK
+        assert torch.isnan(lse[0, 0, 200:]).all() and torch.isnan(o[0, 200:, 0]).all()
+        assert torch.isfinite(lse[0, 0, :200]).all() and torch.isfinite(o[0, :200, 0]).all()
+        assert torch.isfinite(lse[0, 1]).all() and torch.isfinite(o[0, :, 1]).all()
+
+
+@on_gpu
 def test_smaller_calls_on_one_context_and_repeats():
     op = arl2.SoftmaxAttention(4, 700, 900, 128, B=2, H_kv=2)
     for Tq, Tk, F in ((700, 900, 0), (1, 900, 0), (257, 100, 1), (700, 700, 64)):
@@ -349,6 +386,22 @@ def test_local_and_recurrent_branches_train_together():
         # Independent roundings of the bf16 values in a gradient's terms: 3 of half a step each.
         assert (got.double() - ex).norm() <= 3 * torch.finfo(BF).eps / 2 * ex.norm(), name
     assert op.status() == arl2.ARL2_OK
+
+
+# ------------------------------------------------------- the exponential on the FMA pipe
+def test_exp2_poly4():
+    """Its constants are the fitted ones, and it is within 2.7e-6 over the range that is used."""
+    csrc = os.path.join(os.path.dirname(os.path.abspath(arl2.__file__)), "csrc")
+    spec = importlib.util.spec_from_file_location("fit_exp2_poly", os.path.join(csrc, "fit_exp2_poly.py"))
+    fit = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fit)
+    src = open(os.path.join(csrc, "arl2_attn.cuh")).read()
+    body = src[src.index("float2 exp2_poly4(float2 x)"):]
+    pairs = re.findall(r"make_float2\((-?\d+\.\d+)f, (-?\d+\.\d+)f\)", body[: body.index("}")])
+    c = np.array([float(a) for a, b in pairs if a == b and abs(float(a)) < 2][::-1][:5], dtype=np.float32)
+    np.testing.assert_allclose(c, fit.remez(4).astype(np.float32), rtol=2e-7)
+    x = np.linspace(-125, 64, 400_001, dtype=np.float32)
+    assert np.abs(fit.eval_f32(c, x).astype(np.float64) / np.exp2(x.astype(np.float64)) - 1).max() < 2.7e-6
 
 
 # ------------------------------------------------------------------------------- refusals
