@@ -376,8 +376,8 @@ void arl2_attn_destroy(arl2_attn* ctx);
  * a_stride (batch, token, head), its last unused with heads = 0. Inputs may have stride 0;
  * an output's elements must not share memory. da is contiguous. Pointers are aligned to
  * their elements; with heads > 0, x, h, dh and dx to 16 bytes, with strides of a multiple of
- * 16 bytes (otherwise that is only faster). Outputs must not overlap inputs, except that h may be x and dx may be dh (same
- * strides).
+ * 16 bytes (otherwise that is only faster). Outputs must not overlap inputs, except that h may
+ * be x and dx may be dh (same strides).
  * All arithmetic is fp32; h, dx and da are rounded once. da uses the stored (rounded) h.
  * The calls take no context, allocate nothing and hold nothing between calls. A sequence of
  * more than a few hundred tokens is cut into chunks whose gate products and partial sums pass

@@ -123,19 +123,12 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
   }
 };
 
-// A load that stays where it is written: the compiler would otherwise move each next to its use, to
-// save registers, and the loads of a batch would wait for one another.
+// A load of one element that stays where it is written: the compiler would otherwise move each next
+// to its use, to save registers, and the loads of a batch would wait for one another.
 template <typename P>
 __device__ __forceinline__ P load_now(const void* src) {
   P r;
-  if constexpr (sizeof(P) >= 16) {
-    uint4* w = reinterpret_cast<uint4*>(&r);
-#pragma unroll
-    for (size_t i = 0; i < sizeof(P) / 16; ++i)
-      asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "l"(static_cast<const uint4*>(src) + i));
-  } else if constexpr (sizeof(P) == 4) {
+  if constexpr (sizeof(P) == 4) {
     asm volatile("ld.global.u32 %0, [%1];" : "=r"(*reinterpret_cast<uint32_t*>(&r)) : "l"(src));
   } else {
     static_assert(sizeof(P) == 2);
@@ -144,7 +137,7 @@ __device__ __forceinline__ P load_now(const void* src) {
   return r;
 }
 
-// s = g s + x and a *= g, with the paired fp32 operations; one gate (GV = 1) or one per value.
+// s = g s + x with the paired fp32 operations; one gate (GV = 1) or one per value.
 template <int V, int GV>
 __device__ __forceinline__ void advance(float (&s)[V], const float (&g)[GV], const float (&x)[V]) {
   if constexpr (V == 1) {
@@ -668,6 +661,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 struct ScanPlan {
   int lanes, groups, slice, nchunks, warps;
   size_t slice_pairs, chunk_pairs;   // workspace, in (A, X) pairs
+  size_t init_floats;                // behind them, room for a copy of h0
 };
 ScanPlan plan_scan(int B, int T, int C, int V) {
   ScanPlan p{};
@@ -694,6 +688,7 @@ ScanPlan plan_scan(int B, int T, int C, int V) {
     const size_t width = static_cast<size_t>(p.groups) * p.lanes * V;
     p.chunk_pairs = static_cast<size_t>(B) * p.nchunks * width;
     p.slice_pairs = p.chunk_pairs * parts;
+    p.init_floats = static_cast<size_t>(B) * C;
   }
   p.slice = static_cast<int>(slice);
   return p;
@@ -709,6 +704,14 @@ cudaError_t launch(const ScanParams& p, int B, int dev, void* workspace, cudaStr
   a.nchunks = plan.nchunks;
   a.slices = static_cast<float2*>(workspace);
   a.chunks = a.slices + plan.slice_pairs;
+  if (a.init && a.init == a.last && plan.nchunks > 1) {
+    // The final state goes where the initial one stands, which CTAs that start late still have to read.
+    void* copy = a.chunks + plan.chunk_pairs;
+    const cudaError_t e =
+        cudaMemcpyAsync(copy, a.init, plan.init_floats * sizeof(float), cudaMemcpyDeviceToDevice, st);
+    if (e != cudaSuccess) return e;
+    a.init = static_cast<const float*>(copy);
+  }
   const long long ctas = static_cast<long long>(B) * plan.groups * plan.nchunks;
   if (ctas > INT_MAX) return cudaErrorInvalidConfiguration;
   auto* pairs = &arl2_scan_pairs_kernel<X, G, V, kHead, kBack>;
@@ -817,12 +820,12 @@ arl2_status current_device(int* dev) {
 
 size_t workspace_bytes(const arl2_scan_shape& s) {
   // Whether 16 bytes can be accessed at once is known only with the pointers.
-  size_t pairs = 0;
+  size_t bytes = 0;
   for (int V : {1, static_cast<int>(16 / elem(s.dtype))}) {
     const ScanPlan p = plan_scan(s.B, s.T, s.C, V);
-    pairs = std::max(pairs, p.slice_pairs + p.chunk_pairs);
+    bytes = std::max(bytes, (p.slice_pairs + p.chunk_pairs) * sizeof(float2) + p.init_floats * sizeof(float));
   }
-  return pairs * sizeof(float2);
+  return bytes;
 }
 bool needs_workspace(const arl2_scan_shape& s) { return workspace_bytes(s) > 0; }
 
@@ -868,8 +871,8 @@ extern "C" arl2_status arl2_scan_forward(const arl2_scan_fwd* f, arl2_stream str
   p.a_b = as.b, p.a_t = as.t, p.a_h = as.h;
   p.out_b = hs.b, p.out_t = hs.t;
   p.T = s.T, p.C = s.C, p.d = head ? s.C / s.heads : 1;
-  return by_type<false>(p, s.B, dev, f->workspace, static_cast<arl2_dtype>(s.dtype), static_cast<arl2_dtype>(s.gate_dtype), head,
-                        wide, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return by_type<false>(p, s.B, dev, f->workspace, static_cast<arl2_dtype>(s.dtype),
+                        static_cast<arl2_dtype>(s.gate_dtype), head, wide, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ARL2_OK
              : ARL2_ERR_CUDA;
 }
@@ -918,8 +921,8 @@ extern "C" arl2_status arl2_scan_backward(const arl2_scan_bwd* f, arl2_stream st
     p.da_b = static_cast<long long>(s.T) * s.C, p.da_t = s.C;
   }
   p.T = s.T, p.C = s.C, p.d = head ? s.C / s.heads : 1;
-  return by_type<true>(p, s.B, dev, f->workspace, static_cast<arl2_dtype>(s.dtype), static_cast<arl2_dtype>(s.gate_dtype), head,
-                       wide, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return by_type<true>(p, s.B, dev, f->workspace, static_cast<arl2_dtype>(s.dtype),
+                       static_cast<arl2_dtype>(s.gate_dtype), head, wide, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ARL2_OK
              : ARL2_ERR_CUDA;
 }

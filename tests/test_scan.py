@@ -4,9 +4,9 @@ the GPU against a token-by-token loop in 64 bits.
 Error bounds. The kernels work in fp32: every product and sum on the way from an input to an
 output rounds by at most u = 2^-24 relative. A token's gate enters one product of its slice
 and one step of the second scan, and slices (of 8 tokens or more) and chunks are composed once
-each, so an input passes through fewer than 2 T + 80 roundings; the error of h_t is below (2 T + 80) u times the same recurrence
-over absolute values, and a stored value is off by half a step of its type on top
-(eps / 2 relative, and half the smallest subnormal of fp16).
+each, so an input passes through fewer than 2 T + 80 roundings; the error of h_t is below
+(2 T + 80) u times the same recurrence over absolute values, and a stored value is off by half
+a step of its type on top (eps / 2 relative, and half the smallest subnormal of fp16).
 """
 import numpy as np
 import pytest
@@ -206,8 +206,9 @@ def test_steps_equal_the_sequence():
     h, final = arl2.scan_forward(x, a, h0=h0)
     state = h0.clone()
     steps = [arl2.scan_forward(x[:, t:t + 1], a[:, :, t:t + 1], h0=state, final=state)[0] for t in range(40)]
-    spread = loop_forward(x.double().abs().cpu().numpy(), channels(a, 2, 256), h0.double().abs().cpu().numpy(), [40] * 3)
-    ref = loop_forward(x.double().cpu().numpy(), channels(a, 2, 256), h0.double().cpu().numpy(), [40] * 3)
+    X, A, S = x.double().cpu().numpy(), channels(a, 2, 256), h0.double().cpu().numpy()
+    spread = loop_forward(np.abs(X), A, np.abs(S), [40] * 3)
+    ref = loop_forward(X, A, S, [40] * 3)
     close(torch.cat(steps, 1), ref[0], spread[0], 160, torch.bfloat16)
     close(state, ref[1], spread[1], 160, torch.float32)
 
