@@ -16,6 +16,7 @@ struct arl2_attn {
   float* records = nullptr;        // partial records of shared tiles, two per CTA
   float* dq_records = nullptr;     // the dq kernel's
   float* stats = nullptr;          // backward: row statistics
+  void* splits = nullptr;          // the CTAs' splits, where a launch of its own makes them
   unsigned int* err = nullptr;     // the error word, then the backward kernel's two tickets
   unsigned long long timeout_ns = 1000000000ull;
   size_t bytes = 0;
@@ -118,6 +119,7 @@ arl2::AttnArgs args_of(const arl2_attn* c, const arl2_attn_shape* s) {
   a.stats = c->stats;
   a.records = c->records;
   a.dq_records = c->dq_records;
+  a.splits = (s->q_len || s->k_len) && c->B > arl2::kSplitBatches ? c->splits : nullptr;
   a.err = c->err;
   a.tickets = c->err + 1;
   a.timeout_ns = c->timeout_ns;
@@ -158,6 +160,7 @@ arl2_status arl2_attn_create(int B, int H, int H_kv, int max_Tq, int max_Tk, int
   const size_t bh = static_cast<size_t>(B) * H;
   const bool ok = alloc(&c->records, 2 * static_cast<size_t>(sms) * arl2::attn_record_floats(d), &c->bytes) &&
                   alloc(&c->dq_records, 2 * static_cast<size_t>(sms) * arl2::attn_dq_record_floats(d), &c->bytes) &&
+                  alloc(reinterpret_cast<arl2::Split**>(&c->splits), sms, &c->bytes) &&
                   alloc(&c->stats, bh * 2 * tiles(max_Tq, 128) * 128, &c->bytes) && alloc(&c->err, 3, &c->bytes) &&
                   cudaMemset(c->err, 0, sizeof(unsigned int)) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
@@ -246,6 +249,7 @@ void arl2_attn_destroy(arl2_attn* c) {
   cudaFree(c->records);
   cudaFree(c->dq_records);
   cudaFree(c->stats);
+  cudaFree(c->splits);
   cudaFree(c->err);
   delete c;
 }

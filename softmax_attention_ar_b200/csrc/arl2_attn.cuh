@@ -85,7 +85,7 @@ __device__ __forceinline__ long long quick_div(long long x, long long y) {
 }
 
 // Where a CTA's range starts; computed by one warp, read by every role.
-struct Split {
+struct alignas(16) Split {
   long long u0, u1, total;
   int ctas;                  // CTAs that have a range
   int b, h, tile, off;       // of unit u0
@@ -115,8 +115,69 @@ __device__ long long head_units(const AttnMask& m, int b, int group, int* most) 
   return s;
 }
 
-// Whether nothing is cut, and the number of CTAs that get a range otherwise. Few units per CTA cost more in adding up records than they
-// save: at least kMinUnits each, unless the tiles alone are more.
+// The same sum of batch b, by one thread.
+template <typename Tiles>
+__device__ long long thread_units(const AttnMask& m, int b, int group, int* most) {
+  const int ql = q_length(m, b), kl = k_length(m, b), n = Tiles::count(m);
+  if (m.F == 0) {
+    const int v = Tiles::valid(m, ql, kl), u = max(1, Tiles::units(m, 0, ql, kl, group));
+    *most = max(*most, u);
+    return static_cast<long long>(v) * u + (n - v);
+  }
+  long long s = 0;
+  for (int i = 0; i < n; ++i) {
+    const int u = max(1, Tiles::units(m, i, ql, kl, group));
+    s += u;
+    *most = max(*most, u);
+  }
+  return s;
+}
+
+// By one warp, a lane for each batch: the units of all batches and the most that a tile has; and the
+// batch that holds unit *r, which becomes the unit's place in it, with the units of one head.
+template <typename Tiles>
+__device__ long long lane_units(const AttnMask& m, int B, int heads, int group, int* most) {
+  long long total = 0;
+  int top = 1;
+  for (int b = threadIdx.x & 31; b < B; b += 32) total += thread_units<Tiles>(m, b, group, &top) * heads;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  *most = __reduce_max_sync(0xffffffffu, top);
+  return total;
+}
+template <typename Tiles>
+__device__ int lane_batch(const AttnMask& m, int B, int heads, int group, long long* r,
+                                       long long* per_head) {
+  const int lane = threadIdx.x & 31;
+  int top = 1;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const long long mine = b0 + lane < B ? thread_units<Tiles>(m, b0 + lane, group, &top) : 0, w = mine * heads;
+    long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const long long sum = __shfl_sync(0xffffffffu, inc, 31);
+    if (*r < sum) {
+      const int l = __ffs(__ballot_sync(0xffffffffu, *r < inc)) - 1;
+      *per_head = __shfl_sync(0xffffffffu, mine, l);
+      *r -= __shfl_sync(0xffffffffu, inc - w, l);
+      return b0 + l;
+    }
+    *r -= sum;
+  }
+  return B;   // not reached: r is below the sum of all
+}
+
+// With lengths, going through the batches one by one takes a CTA 0.3 us each. More batches than this
+// are gone through by lanes in a launch of its own, which writes every CTA's split to memory: 64
+// batches of 128 tokens and 12 heads 89 -> 49 us (37 without lengths). Where the kernels did that
+// themselves, the code alone made every small call 2 us longer.
+constexpr int kSplitBatches = 4;
+
+// Whether nothing is cut, and the number of CTAs that get a range otherwise. Few units per CTA cost
+// more in adding up records than they save: at least kMinUnits each, unless the tiles alone are more.
 constexpr int kMinUnits = 4;
 __host__ __device__ inline bool split_whole(long long tiles, long long total, long long most, long long grid,
                                             int cut_cost) {
@@ -130,16 +191,22 @@ __host__ __device__ inline long long split_ctas(long long tiles, long long total
   return n > 1 ? n : 1;
 }
 
-template <typename Tiles>
+// kLanes: for many batches with lengths.
+template <typename Tiles, bool kLanes = false>
 __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c, int grid, Split* out) {
   const int lane = threadIdx.x & 31;
   const bool ragged = m.q_len || m.k_len;
   const int n = Tiles::count(m);
+  // A lane sums up a batch of its own, unless the tiles are more.
+  const bool by_lane =
+      kLanes && ragged && (m.F == 0 || static_cast<long long>((B + 31) / 32) * n <= 8ll * B);
   long long total = 0, per_head = 0;
   int most = 1;
   if (!ragged) {
     per_head = head_units<Tiles>(m, 0, group, &most);
     total = per_head * heads * B;
+  } else if (by_lane) {
+    total = lane_units<Tiles>(m, B, heads, group, &most);
   } else {
     for (int b = 0; b < B; ++b) total += head_units<Tiles>(m, b, group, &most) * heads;
   }
@@ -168,6 +235,8 @@ __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c
       const long long per_batch = per_head * heads;
       s.b = static_cast<int>(quick_div(r, per_batch));
       r -= s.b * per_batch;
+    } else if (by_lane) {
+      s.b = lane_batch<Tiles>(m, B, heads, group, &r, &per_head);
     } else {
       for (; s.b < B; ++s.b) {
         per_head = head_units<Tiles>(m, s.b, group, &most);
@@ -208,6 +277,18 @@ __device__ void make_split(const AttnMask& m, int B, int heads, int group, int c
     }
   }
   if (lane == 0) *out = s;
+}
+// The split of CTA c: from `made` (see kSplitBatches) or computed here.
+template <typename Tiles>
+__device__ __forceinline__ void get_split(const AttnMask& m, int B, int heads, int group, int c, int grid,
+                                          const Split* made, Split* out) {
+  if (made) {
+    const int lane = threadIdx.x & 31;
+    const uint4* src = reinterpret_cast<const uint4*>(made + min(c, grid - 1));
+    if (lane < static_cast<int>(sizeof(Split) / 16)) reinterpret_cast<uint4*>(out)[lane] = __ldcg(src + lane);
+  } else {
+    make_split<Tiles>(m, B, heads, group, c, grid, out);
+  }
 }
 
 // One segment: units [kb, ke) of a tile.
@@ -369,19 +450,18 @@ __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint32_t a_tile, uin
   } else {
     const uint64_t a0 = desc_kmajor(a_tile, 0), b0 = desc_kmajor(b_tile, 0);
 #pragma unroll
-    for (int s = 0; s < TileOf<D>::kSteps; ++s) mma_bf16(d_tmem, a0 + kmajor_step16(s), b0 + kmajor_step16(s), idesc, s > 0);
+    for (int s = 0; s < TileOf<D>::kSteps; ++s)
+      mma_bf16(d_tmem, a0 + kmajor_step16(s), b0 + kmajor_step16(s), idesc, s > 0);
   }
 }
-// D[tmem] (+)= P B over 128 rows: P packed in TMEM (columns a + 8 s, the second half of the
-// steps kSplit columns further than that), B a tile of 128 rows (MN-major).
-template <int kSplit>
+// D[tmem] (+)= P B over 128 rows: P packed in TMEM in two parts (columns a + 8 s, and from a + 64 on
+// for the second four steps), B a tile of 128 rows (MN-major).
 __device__ __forceinline__ void mma_over_rows(uint32_t d_tmem, uint32_t a, uint32_t b_tile, uint32_t idesc,
                                               uint32_t acc) {
-  constexpr uint32_t col[8] = {0, 8, 16, 24, 32 + kSplit, 40 + kSplit, 48 + kSplit, 56 + kSplit};
+  constexpr uint32_t col[8] = {0, 8, 16, 24, 64, 72, 80, 88};
   mma8_ts(d_tmem, a, col, desc_mnmajor(b_tile, 0), idesc, acc);
 }
-
-// Steps [4 kHalf, 4 kHalf + 4) of it, with kSplit = 0.
+// Steps [4 kHalf, 4 kHalf + 4) of it, P in one part (columns a + 8 s).
 template <int kHalf>
 __device__ __forceinline__ void mma_over_half_rows(uint32_t d_tmem, uint32_t a, uint32_t b_tile, uint32_t idesc,
                                                    uint32_t acc) {

@@ -198,7 +198,7 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
       prefetch_tmap(&tm_g);
     }
     __syncwarp();
-    make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, cta, nctas, &shared->split);
+    get_split<KeyTiles>(a.mask, a.B, a.Hkv, group, cta, nctas, static_cast<const Split*>(a.splits), &shared->split);
   }
   if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
   tc_fence_before();
@@ -312,7 +312,7 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
         if (!ok) break;
         tc_fence_after();
         if (lead) {
-          mma_over_rows<32>(c_dv, c_s, g_at(n), id_d, acc);
+          mma_over_rows(c_dv, c_s, g_at(n), id_d, acc);
           if (more) {
             mma_over_d<D>(c_s, k_tile, q_at(n + 1), id_s);
             mma_commit(bar(kKSFull));
@@ -324,7 +324,7 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
         if (!ok) break;
         tc_fence_after();
         if (lead) {
-          mma_over_rows<32>(c_dk, c_dp, q_at(n), id_d, acc);
+          mma_over_rows(c_dk, c_dp, q_at(n), id_d, acc);
           if (more) {
             mma_over_d<D>(c_dp, v_tile, g_at(n + 1), id_s);
             mma_commit(bar(kKDFull));
@@ -428,7 +428,8 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
             const float2 d0 = __fmul2_rn(
                 p[k / 2], __fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(e.x, e.y)));
             const float2 d1 = __fmul2_rn(
-                p[k / 2 + 1], __fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(e.z, e.w)));
+                p[k / 2 + 1],
+                __fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(e.z, e.w)));
             w[k / 2] = pack2<kHalf>(d0.x, d0.y);
             w[k / 2 + 1] = pack2<kHalf>(d1.x, d1.y);
           }
@@ -510,7 +511,9 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMa
       prefetch_tmap(&tm_g);
     }
     __syncwarp();
-    make_split<QTiles>(a.mask, a.B, a.H, 1, cta, nctas, &shared->split);
+    // The dq kernel's splits stand behind those of the gridDim.x - nctas others.
+    const Split* made = static_cast<const Split*>(a.splits);
+    get_split<QTiles>(a.mask, a.B, a.H, 1, cta, nctas, made ? made + (gridDim.x - nctas) : nullptr, &shared->split);
   }
   if (warp == 1) tmem_alloc(smem_u32(&shared->tmem), 512);
   tc_fence_before();
@@ -609,7 +612,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMa
             mma_commit(bar(kQDFull));
             mma_commit(bar(kQVEmpty + (n + 1) % 2));
           }
-          mma_over_rows<32>(c_dq, tmem + 128u * (n & 1), k_at(n), id_d, u > 0);
+          mma_over_rows(c_dq, tmem + 128u * (n & 1), k_at(n), id_d, u > 0);
           mma_commit(bar(kQKEmpty + n % 3));
         }
         __syncwarp();
@@ -763,16 +766,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // (c, y) takes 32 columns of the tile at the start of CTA c's range; y < D / 32: of dv, then of
 // dk, then, in the dq kernel's split, of dq.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const __grid_constant__ AttnArgs a, int n_dkv, int n_dq) {
+__global__ void __launch_bounds__(kRows, 4)
+    arl2_attn_bwd_combine_kernel(const __grid_constant__ AttnArgs a, int n_dkv, int n_dq) {
   __shared__ Split split;
   constexpr int kParts = D / 32;
   const int c = static_cast<int>(blockIdx.x) + 1, r = threadIdx.x, what = blockIdx.y / kParts;
   const int k0 = 32 * (blockIdx.y % kParts), group = a.H / a.Hkv;
   if (threadIdx.x < 32) {
+    const Split* made = static_cast<const Split*>(a.splits);
     if (what < 2)
-      make_split<KeyTiles>(a.mask, a.B, a.Hkv, group, c, n_dkv, &split);
+      get_split<KeyTiles>(a.mask, a.B, a.Hkv, group, c, n_dkv, made, &split);
     else
-      make_split<QTiles>(a.mask, a.B, a.H, 1, c, n_dq, &split);
+      get_split<QTiles>(a.mask, a.B, a.H, 1, c, n_dq, made ? made + n_dkv : nullptr, &split);
   }
   __syncthreads();
   const Split sp = split;
@@ -780,7 +785,8 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const _
   const long long first = sp.u0 - sp.off;
   if (sp.whole || c >= sp.ctas || sp.off == 0 || unit_owner(sp, first) != c - 1) return;
   const int ql = q_length(a.mask, sp.b), kl = k_length(a.mask, sp.b);
-  const int units = what < 2 ? KeyTiles::units(a.mask, sp.tile, ql, kl, group) : QTiles::units(a.mask, sp.tile, ql, kl, 1);
+  const int units =
+      what < 2 ? KeyTiles::units(a.mask, sp.tile, ql, kl, group) : QTiles::units(a.mask, sp.tile, ql, kl, 1);
   const int c1 = unit_owner(sp, first + max(1, units) - 1);
   const int row = sp.tile * kRows + r;
   float y[32];
@@ -799,12 +805,23 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_bwd_combine_kernel(const _
     store32<kHalf>(out.ptr + sp.b * out.sb + row * out.st + sp.h * out.sh + k0, y);
 }
 
+// Block c writes the split of CTA c of those that compute dk and dv, and behind them dq.
+__global__ void __launch_bounds__(32) arl2_attn_bwd_split_kernel(const __grid_constant__ AttnArgs a, int n_dkv) {
+  const int i = static_cast<int>(blockIdx.x);
+  Split* out = static_cast<Split*>(a.splits) + i;
+  if (i < n_dkv)
+    make_split<KeyTiles, true>(a.mask, a.B, a.Hkv, a.H / a.Hkv, i, n_dkv, out);
+  else
+    make_split<QTiles, true>(a.mask, a.B, a.H, 1, i - n_dkv, static_cast<int>(gridDim.x) - n_dkv, out);
+}
+
 // Also loads the kernels, so that a first call inside a stream capture finds them there.
 template <int D, bool kHalf>
 cudaError_t setup() {
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, arl2_attn_prep_kernel<kHalf>);
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, arl2_attn_bwd_combine_kernel<D, kHalf>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, arl2_attn_bwd_split_kernel);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(arl2_attn_bwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(bwd_smem<D>()));
@@ -814,8 +831,10 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
                    const AttnPrepArgs& prep, const AttnArgs& a, int ctas, bool combine, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.B) * ((a.mask.Tq + kRows - 1) / kRows * kRows) * a.H;
   const unsigned blocks = static_cast<unsigned>((rows * (D / 8) + 255) / 256);
-  cudaError_t e = launch_chained(arl2_attn_prep_kernel<kHalf>, dim3(blocks), 256, 0, st, false, prep);
   const int n_dkv = attn_dkv_ctas(ctas), n_dq = ctas - n_dkv;
+  cudaError_t e = cudaSuccess;
+  if (a.splits) e = launch_chained(arl2_attn_bwd_split_kernel, dim3(ctas), 32, 0, st, false, a, n_dkv);
+  if (e == cudaSuccess) e = launch_chained(arl2_attn_prep_kernel<kHalf>, dim3(blocks), 256, 0, st, false, prep);
   if (e == cudaSuccess)
     e = launch_chained(arl2_attn_bwd_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a,
                        n_dkv);

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       prefetch_tmap(&tm_v);
     }
     __syncwarp();
-    make_split<FwdTiles>(a.mask, a.B, a.H, 1, blockIdx.x, gridDim.x, split);
+    get_split<FwdTiles>(a.mask, a.B, a.H, 1, blockIdx.x, gridDim.x, static_cast<const Split*>(a.splits), split);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int k = 0; k < 2 * n; ++k, ++r) {
         // K and V by turns; in a narrow tile the keys run one tile ahead.
         const int kv = tiles == 2 ? k & 1 : k < 2 ? n == 1 && k == 1 : k == 2 * n - 1 || !(k & 1);
-        const int t = sg.kb + (tiles == 2 ? k >> 1 : kv ? (k == 2 * n - 1 ? n - 1 : k / 2 - 1) : k < 2 ? k : (k + 1) / 2);
+        const int t =
+            sg.kb + (tiles == 2 ? k >> 1 : kv ? (k == 2 * n - 1 ? n - 1 : k / 2 - 1) : k < 2 ? k : (k + 1) / 2);
         const uint32_t st = r % kRing;
         ok = r < kRing || mbar_wait_warp(bar(kFEmpty + st), (r / kRing - 1) & 1, g);
         if (!ok) break;
@@ -504,7 +505,8 @@ template <int D, bool kHalf>
 __global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ Split split;
   const int c = static_cast<int>(blockIdx.x) + 1, r = threadIdx.x;
-  if (threadIdx.x < 32) make_split<FwdTiles>(a.mask, a.B, a.H, 1, c, gridDim.x + 1, &split);
+  if (threadIdx.x < 32)
+    get_split<FwdTiles>(a.mask, a.B, a.H, 1, c, gridDim.x + 1, static_cast<const Split*>(a.splits), &split);
   __syncthreads();
   const Split sp = split;
   griddep_wait();   // the records; every block, so that this grid ends after the one before it
@@ -548,11 +550,17 @@ __global__ void __launch_bounds__(kRows, 4) arl2_attn_fwd_combine_kernel(const _
         sees ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Block c writes the split of CTA c.
+__global__ void __launch_bounds__(32) arl2_attn_fwd_split_kernel(const __grid_constant__ AttnArgs a) {
+  make_split<FwdTiles, true>(a.mask, a.B, a.H, 1, blockIdx.x, gridDim.x, static_cast<Split*>(a.splits) + blockIdx.x);
+}
+
 // Also loads the kernels, so that a first call inside a stream capture finds them there.
 template <int D, bool kHalf>
 cudaError_t setup() {
   cudaFuncAttributes attr;
-  const cudaError_t e = cudaFuncGetAttributes(&attr, arl2_attn_fwd_combine_kernel<D, kHalf>);
+  cudaError_t e = cudaFuncGetAttributes(&attr, arl2_attn_fwd_combine_kernel<D, kHalf>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, arl2_attn_fwd_split_kernel);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(arl2_attn_fwd_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(fwd_smem<D>()));
@@ -560,8 +568,10 @@ cudaError_t setup() {
 template <int D, bool kHalf>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int ctas,
                    bool combine, cudaStream_t st) {
-  const cudaError_t e =
-      launch_chained(arl2_attn_fwd_kernel<D, kHalf>, dim3(ctas), kFwdThreads, fwd_smem<D>(), st, false, q, k, v, a);
+  cudaError_t e = cudaSuccess;
+  if (a.splits) e = launch_chained(arl2_attn_fwd_split_kernel, dim3(ctas), 32, 0, st, false, a);
+  if (e == cudaSuccess)
+    e = launch_chained(arl2_attn_fwd_kernel<D, kHalf>, dim3(ctas), kFwdThreads, fwd_smem<D>(), st, false, q, k, v, a);
   if (e != cudaSuccess || !combine || ctas < 2) return e;
   return launch_chained(arl2_attn_fwd_combine_kernel<D, kHalf>, dim3(ctas - 1, 2 * (D / 32)), kRows, 0, st, true, a);
 }
@@ -582,9 +592,11 @@ cudaError_t launch_attn_fwd(int d, bool half, const CUtensorMap& q, const CUtens
                             const AttnArgs& a, int ctas, bool combine, cudaStream_t st) {
   if (half)
     return d == 32 ? launch<32, true>(q, k, v, a, ctas, combine, st)
-                   : d == 64 ? launch<64, true>(q, k, v, a, ctas, combine, st) : launch<128, true>(q, k, v, a, ctas, combine, st);
+                   : d == 64 ? launch<64, true>(q, k, v, a, ctas, combine, st)
+                            : launch<128, true>(q, k, v, a, ctas, combine, st);
   return d == 32 ? launch<32, false>(q, k, v, a, ctas, combine, st)
-                 : d == 64 ? launch<64, false>(q, k, v, a, ctas, combine, st) : launch<128, false>(q, k, v, a, ctas, combine, st);
+                 : d == 64 ? launch<64, false>(q, k, v, a, ctas, combine, st)
+                           : launch<128, false>(q, k, v, a, ctas, combine, st);
 }
 
 }  // namespace arl2

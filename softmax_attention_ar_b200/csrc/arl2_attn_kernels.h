@@ -25,6 +25,7 @@ struct AttnArgs {
   const float* stats;     // backward: [B H][2][Tq rounded up to 128]: -lse in log2 units, then -delta
   float* records;         // partial records, two per CTA
   float* dq_records;      // the dq kernel's
+  void* splits;           // the CTAs' splits, written by a launch of its own, or null: each computes its own
   unsigned int* tickets;  // backward: ranges handed out, [dk and dv, dq]
   unsigned int* err;
   unsigned long long timeout_ns;
@@ -42,7 +43,8 @@ struct AttnPrepArgs {
   int B, H, Tq, d;
 };
 
-__host__ __device__ constexpr size_t attn_record_floats(int d) { return 2ull * 128 * d + 4 * 128; }   // forward; dk and dv
+// Forward, and dk with dv.
+__host__ __device__ constexpr size_t attn_record_floats(int d) { return 2ull * 128 * d + 4 * 128; }
 __host__ __device__ constexpr size_t attn_dq_record_floats(int d) { return 128ull * d; }
 cudaError_t attn_fwd_setup();
 cudaError_t attn_bwd_setup();

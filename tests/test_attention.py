@@ -164,13 +164,24 @@ def test_lengths(d, dtype, frame_len):
 
 
 @on_gpu
+@pytest.mark.parametrize("B,T,H,frame_len", [(70, 150, 2, 0), (33, 300, 1, 16), (1, 2500, 2, 200), (2, 2600, 1, 1)])
+def test_padded_batches(B, T, H, frame_len):
+    # Batches by lanes of the warp that cuts the work, several rounds of them, or one after another.
+    g = np.random.default_rng(B)
+    q_len, k_len = (g.integers(0, T + 1, B).tolist() for _ in range(2))
+    q_len[0], k_len[0] = T - 3, T - 70
+    check(B, T, T, H, 1, 64, BF, q_len=q_len, k_len=k_len, frame_len=frame_len, seed=B)
+
+
+@on_gpu
 def test_every_row_empty():
     check(2, 70, 90, 2, 2, 64, BF, k_len=[0, 0])
     check(1, 70, 90, 2, 2, 64, BF, frame_len=10, q_start=-200)
 
 
 @on_gpu
-@pytest.mark.parametrize("B,T,H,Hkv,d,dtype", [(1, 1560, 12, 12, 128, BF), (1, 1560, 4, 2, 64, HF), (2, 2048, 3, 1, 32, BF)])
+@pytest.mark.parametrize("B,T,H,Hkv,d,dtype", [
+    (1, 1560, 12, 12, 128, BF), (1, 1560, 4, 2, 64, HF), (2, 2048, 3, 1, 32, BF)])
 def test_frame_sizes(B, T, H, Hkv, d, dtype):
     check(B, T, T, H, Hkv, d, dtype)
 
