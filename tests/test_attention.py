@@ -479,3 +479,26 @@ def test_c_entry_refuses_without_a_gpu():
     assert lib.arl2_attn_forward(None, f, None) == bad
     assert lib.arl2_attn_get_status(None) == bad and lib.arl2_attn_memory_bytes(None) == 0
     lib.arl2_attn_destroy(None)
+
+
+@on_gpu
+def test_captured_padded_batch_equals_eager():
+    # Lengths that change between replays: the captured launches cut the work anew each time.
+    B, T, H, d = 40, 150, 2, 64
+    q, k, v, do = make(B, T, T, H, H, d, BF, seed=5)
+    op = arl2.SoftmaxAttention(H, T, T, d, B=B)
+    n = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    run = lambda: (lambda o, lse: (o, lse) + op.backward(do, q, k, v, o, lse, q_len=n, k_len=n))(
+        *op.forward(q, k, v, q_len=n, k_len=n))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for seed in (1, 2):
+        n.copy_(torch.from_numpy(np.random.default_rng(seed).integers(0, T + 1, B).astype(np.int32)))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        assert all(torch.equal(x, y) for x, y in zip(kept, run()))
+    assert op.status() == arl2.ARL2_OK
