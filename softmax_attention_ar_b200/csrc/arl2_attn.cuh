@@ -353,13 +353,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return pack_bf16x2(lo, hi);
   }
 }
+// Maxima that keep a NaN.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 // 2^x for a pair on the FMA pipe with paired fp32 operations, max relative error 2.7e-6 for x in
-// [-125, 64] (at least 2^-126 below; a NaN gives a large value). Method as exp2_poly in
-// arl2_device.cuh: x = n + f with n = round(x), then a degree-4 polynomial for 2^f with
+// [-125, 64] (at least 2^-126 below; a NaN gives 3.4e38, which is infinite in 16 bits). Method as
+// exp2_poly in arl2_device.cuh: x = n + f with n = round(x), then a degree-4 polynomial for 2^f with
 // equioscillating relative error (fit_exp2_poly.py) and n added to the exponent field.
 __device__ __forceinline__ float2 exp2_poly4(float2 x) {
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
+  x.x = fmax_nan(x.x, -126.f);
+  x.y = fmax_nan(x.y, -126.f);
   const float2 t = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
   const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
   const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
@@ -374,12 +385,6 @@ __device__ __forceinline__ float2 exp2_poly4(float2 x) {
 __host__ __device__ constexpr bool fma_pair(uint32_t pairs, int j) { return (pairs >> (j & 7)) & 1u; }
 __device__ __forceinline__ float2 exp2_pair(float2 x, bool on_fma) {
   return on_fma ? exp2_poly4(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
-}
-// Three-input maximum that keeps a NaN.
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 // kind::f16 instruction descriptor for fp16 or bf16 operands (both of one type).
 template <bool kHalf>

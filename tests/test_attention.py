@@ -251,6 +251,24 @@ def test_nan_and_infinity_in_seen_places_stay_in_their_rows():
 
 
 @on_gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_a_nan_query_shows_in_all_its_gradients(dtype):
+    # Whichever column it is in: dv of every key that it sees, dk as well, and its own dq.
+    T, H, d, F = 150, 2, 64, 50
+    op = arl2.SoftmaxAttention(H, T, T, d, dtype=dtype)
+    for i in range(60, 76):
+        q, k, v, do = make(1, T, T, H, H, d, dtype, seed=11)
+        q[0, i, 0, 3] = float("nan")
+        o, lse = op.forward(q, k, v, frame_len=F)
+        dq, dk, dv = op.backward(do, q, k, v, o, lse, frame_len=F)
+        assert op.status() == arl2.ARL2_OK
+        assert torch.isnan(o[0, i, 0]).all() and torch.isnan(dq[0, i, 0]).all()
+        assert not torch.isfinite(dv[0, :100, 0]).any() and not torch.isfinite(dk[0, :100, 0, 3]).any()
+        assert torch.isfinite(dv[0, 100:, 0]).all()
+        assert all(torch.isfinite(t[0, :, 1]).all() for t in (o, dq, dk, dv))
+
+
+@on_gpu
 def test_smaller_calls_on_one_context_and_repeats():
     op = arl2.SoftmaxAttention(4, 700, 900, 128, B=2, H_kv=2)
     for Tq, Tk, F in ((700, 900, 0), (1, 900, 0), (257, 100, 1), (700, 700, 64)):
