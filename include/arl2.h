@@ -302,10 +302,10 @@ void arl2_kvcache_destroy(arl2_kvcache* c);
  * Key j is visible to query i if i < q_len[b], j < k_len[b] and, with frame_len > 0,
  *   j < (floor((i + q_start) / frame_len) + 1) * frame_len:
  * a query sees its own frame and the frames before it (frame_len = 1: causal), q_start being the
- * place of query 0 among the keys. A row that sees nothing has o = 0, lse = -inf and dq = 0;
- * dk and dv are 0 where nothing sees the key. Rows of q, o and do behind q_len, and of k and v
- * behind k_len, may hold anything: they reach no result, and the rows of o, dq, dk and dv
- * there are 0, those of lse -inf.
+ * place of query 0 among the keys. A row that sees nothing has o = 0, lse = -inf and dq = 0 (so
+ * has one whose scores are all -inf, but for dq); dk and dv are 0 where nothing sees the key.
+ * Rows of q, o and do behind q_len, and of k and v behind k_len, may hold anything: they reach
+ * no result, and the rows of o, dq, dk and dv there are 0, those of lse -inf.
  * q, o, do, dq: [B, Tq, H, d]; k, v, dk, dv: [B, Tk, H_kv, d], of the context's type (bf16 or
  * fp16), d in {32, 64, 128}, given as a pointer and strides in elements (batch, token, head),
  * elements of a head adjacent: pointers 16-byte aligned, strides positive multiples of 8 (any

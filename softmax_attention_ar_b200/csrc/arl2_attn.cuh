@@ -365,12 +365,13 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   return d;
 }
 // 2^x for a pair on the FMA pipe with paired fp32 operations, max relative error 2.7e-6 for x in
-// [-125, 64] (at least 2^-126 below; a NaN gives 3.4e38, which is infinite in 16 bits). Method as
-// exp2_poly in arl2_device.cuh: x = n + f with n = round(x), then a degree-4 polynomial for 2^f with
-// equioscillating relative error (fit_exp2_poly.py) and n added to the exponent field.
+// [-125, 64]. Method as exp2_poly in arl2_device.cuh: x = n + f with n = round(x), then a degree-4
+// polynomial for 2^f with equioscillating relative error (fit_exp2_poly.py). Here it is multiplied by
+// 2^n, made from n's bits, in place of adding n to the exponent field: that keeps a NaN, and at the
+// lower end (n = -127, where the bits give 0) the result is exactly 0, as for -inf on the MUFU unit.
 __device__ __forceinline__ float2 exp2_poly4(float2 x) {
-  x.x = fmax_nan(x.x, -126.f);
-  x.y = fmax_nan(x.y, -126.f);
+  x.x = fmax_nan(x.x, -127.f);
+  x.y = fmax_nan(x.y, -127.f);
   const float2 t = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
   const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
   const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
@@ -378,8 +379,8 @@ __device__ __forceinline__ float2 exp2_poly4(float2 x) {
   p = __ffma2_rn(p, f, make_float2(0.2402474433f, 0.2402474433f));
   p = __ffma2_rn(p, f, make_float2(0.6931217909f, 0.6931217909f));
   p = __ffma2_rn(p, f, make_float2(0.9999992847f, 0.9999992847f));
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+  return __fmul2_rn(p, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                                   __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
 }
 // Column pairs, of every 8, that take it; the others go to the MUFU unit.
 __host__ __device__ constexpr bool fma_pair(uint32_t pairs, int j) { return (pairs >> (j & 7)) & 1u; }

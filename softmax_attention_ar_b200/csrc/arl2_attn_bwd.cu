@@ -6,7 +6,7 @@
 //
 // The tensor cores bound it. Launches, each a programmatic dependent of the one before:
 //   - arl2_attn_prep_kernel: -delta, and -lse in log2 units (-inf where a row sees nothing or lies
-//     behind its length: P is then 0 or next to it), padded to whole 128-row tiles;
+//     behind its length: P is then 0), padded to whole 128-row tiles;
 //   - arl2_attn_bwd_kernel, some of whose CTAs compute dk and dv (dkv_cta): a tile is 128 keys of
 //     one key head and runs over the query tiles of every query head that shares the head, so the
 //     heads' sum stays in the accumulators; and the others dq (dq_cta): a tile is 128 query rows of

@@ -385,13 +385,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             e[k] = exp2_pair(
                 __ffma2_rn(make_float2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), sc, sh),
                 fma_pair(kFwdFmaPairs, k));
-          if (masked) {   // exactly 0, where the FMA pipe's 2^-inf is only next to it
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              if (32 * q + 2 * k >= seen) e[k].x = 0.f;
-              if (32 * q + 2 * k + 1 >= seen) e[k].y = 0.f;
-            }
-          }
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {

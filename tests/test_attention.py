@@ -520,3 +520,35 @@ def test_captured_padded_batch_equals_eager():
         kept = [t.clone() for t in got]
         assert all(torch.equal(x, y) for x, y in zip(kept, run()))
     assert op.status() == arl2.ARL2_OK
+
+
+# ------------------------------------------------------------------------- special values
+@on_gpu
+@pytest.mark.parametrize("Tq,Tk", [(300, 300), (70, 300), (1, 5), (200, 20000)])
+def test_rows_that_see_only_scores_of_minus_infinity(Tq, Tk):
+    # Whole tiles, narrow ones and tiles cut between CTAs: exp(-inf) is exactly 0, whichever pipe
+    # computes it, so such a row is one that sees nothing.
+    H, d = 2, 64
+    q, k, v, do = make(1, Tq, Tk, H, H, d, BF, seed=12)
+    k[0, :, 0, 0] = -float("inf")
+    q[0, :, 0, 0] = q[0, :, 0, 0].abs() + 0.1
+    op = arl2.SoftmaxAttention(H, Tq, Tk, d)
+    o, lse = op.forward(q, k, v)
+    assert op.status() == arl2.ARL2_OK
+    assert torch.isneginf(lse[0, 0]).all() and (o[0, :, 0] == 0).all()
+    assert torch.isfinite(lse[0, 1]).all() and torch.isfinite(o[0, :, 1]).all()
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_a_nan_query_makes_dv_nan(dtype):
+    # A NaN, not an infinity, whichever column the row is in.
+    T, H, d, F = 150, 1, 64, 50
+    op = arl2.SoftmaxAttention(H, T, T, d, dtype=dtype)
+    for i in range(60, 76):
+        q, k, v, do = make(1, T, T, H, H, d, dtype, seed=13)
+        q[0, i, 0, 3] = float("nan")
+        o, lse = op.forward(q, k, v, frame_len=F)
+        dq, dk, dv = op.backward(do, q, k, v, o, lse, frame_len=F)
+        assert op.status() == arl2.ARL2_OK
+        assert torch.isnan(dv[0, :100, 0]).all() and torch.isnan(dk[0, :100, 0]).all()
