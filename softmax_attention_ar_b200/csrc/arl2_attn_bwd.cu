@@ -384,7 +384,9 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
         ok = mbar_wait_warp(bar(kKSFull), n & 1, g);
         if (!ok) break;
         tc_fence_after();
-        const int hidden = row0 - (i * kRows + 64 * wg);   // this thread's columns below it see nothing
+        // Of this thread's columns, those below `hidden` do not see the key. Those from `rows` on are behind
+        // the length: q reads as 0 there, and 0 times an infinite key is no score.
+        const int hidden = row0 - (i * kRows + 64 * wg), rows = sg.ql - (i * kRows + 64 * wg);
         float2 p[32];
         {
           uint32_t s[2][32];
@@ -399,11 +401,11 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
             p[k / 2 + 1] = exp2_pair(__ffma2_rn(x1, sc, make_float2(l.z, l.w)), fma_pair(kBwdFmaPairs, k / 2 + 1));
           }
         }
-        if (__any_sync(0xffffffffu, hidden > 0)) {
+        if (__any_sync(0xffffffffu, hidden > 0 || rows < 64)) {
 #pragma unroll
           for (int k = 0; k < 64; k += 2) {
-            if (k < hidden) p[k / 2].x = 0.f;
-            if (k + 1 < hidden) p[k / 2].y = 0.f;
+            if (k < hidden || k >= rows) p[k / 2].x = 0.f;
+            if (k + 1 < hidden || k + 1 >= rows) p[k / 2].y = 0.f;
           }
         }
         {

@@ -552,3 +552,22 @@ def test_a_nan_query_makes_dv_nan(dtype):
         dq, dk, dv = op.backward(do, q, k, v, o, lse, frame_len=F)
         assert op.status() == arl2.ARL2_OK
         assert torch.isnan(dv[0, :100, 0]).all() and torch.isnan(dk[0, :100, 0]).all()
+
+
+@on_gpu
+@pytest.mark.parametrize("Tq,q_len", [(256, None), (300, None), (300, 200), (1, None), (2000, None)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_rows_behind_the_last_query_reach_no_gradient(Tq, q_len, dtype):
+    # Keys of -inf: the rows that fill up the last query tile must not meet them as 0 * inf. Every
+    # score is -inf, every probability 0.
+    H, Tk, d = 2, 300, 64
+    q, k, v, do = make(1, Tq, Tk, H, H, d, dtype, seed=12)
+    k[0, :, 0, 0] = -float("inf")
+    q[0, :, 0, 0] = q[0, :, 0, 0].abs() + 0.1
+    n = None if q_len is None else torch.tensor([q_len], dtype=torch.int32, device="cuda")
+    op = arl2.SoftmaxAttention(H, Tq, Tk, d, dtype=dtype)
+    o, lse = op.forward(q, k, v, q_len=n)
+    dq, dk, dv = op.backward(do, q, k, v, o, lse, q_len=n)
+    assert op.status() == arl2.ARL2_OK
+    assert (dv[0, :, 0] == 0).all() and (dk[0, :, 0] == 0).all()
+    assert all(torch.isfinite(t[0, :, 1]).all() for t in (o, dq, dk, dv))
