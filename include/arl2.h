@@ -360,9 +360,12 @@ void arl2_attn_destroy(arl2_attn* ctx);
  * and its backward pass, for dh the gradient of h and dfinal that of the last state,
  *   lam_t = dh_t + a_{t+1} lam_{t+1},   lam_{T-1} = dh_{T-1} + dfinal,
  *   dx_t = lam_t,   da_t = lam_t h_{t-1},   dh0 = a_0 lam_0.
- * The gates a are given as values (any real number: 0 forgets, 1 keeps), either one per
+ * The gates a are given as values (0 forgets, 1 keeps; any real number), either one per
  * channel and token, or one per head and token in the layout of arl2_frame_gates' alpha. With
- * T = 1 the forward call is the serving step: h0 in, final_state out.
+ * T = 1 the forward call is the serving step: h0 in, final_state out. Parts of a sequence are
+ * joined by the products of their gates: one above fp32's range acts as infinite and one below
+ * 2^-126 as 0, even if other gates lead back, but a state of 0 stays 0 and a gate of 0 forgets.
+ * Gates of at most 1 in absolute value never come to that.
  *
  * Shapes: x, h, dh, dx [B, T, C] of type dtype (bf16, fp16 or fp32). heads = 0: gates
  * [B, T, C] of type dtype or fp32. heads > 0: gates fp32 [B, heads, T], each for the d =

@@ -172,8 +172,16 @@ __device__ __forceinline__ void scale_by(float (&a)[GV], const float (&g)[GV]) {
 #pragma unroll
   for (int i = 0; i < GV; ++i) a[i] *= g[i];
 }
-// A state moved past a pair.
-__device__ __forceinline__ float past(float2 pair, float s) { return fmaf(pair.x, s, pair.y); }
+// Products of gates above 1 over many tokens may pass fp32's range where the state they meet does not:
+// a state of 0 stays 0, and a gate of 0 makes the product 0, where inf * 0 would be a NaN. Of the gates
+// themselves, only a NaN does that.
+__device__ __forceinline__ float past(float2 pair, float s) {   // a state moved past a pair
+  return s == 0.f && pair.x == pair.x ? pair.y : fmaf(pair.x, s, pair.y);
+}
+__device__ __forceinline__ float gate_product(float x, float y) {
+  return (x == 0.f && y == y) || (y == 0.f && x == x) ? 0.f : x * y;
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 // A store of data that this call does not read again: evict-first in L2.
 template <typename P>
@@ -409,6 +417,8 @@ struct Place {
     }
   }
   // The (A, X) of this slice, after start<true>(): from the end, X = sum of x times the gates behind.
+  // Where their product passed fp32's range (rare), X was made of it too: then once more in the order
+  // of the recurrence, in which X stays a state.
   __device__ __forceinline__ void pairs(const ScanParams& a, float2 (&pair)[V]) const {
     float A[GV], S[V];
 #pragma unroll
@@ -425,6 +435,29 @@ struct Place {
         scale_by(A, gf);
       }
     });
+    bool in_range = true;
+#pragma unroll
+    for (int v = 0; v < GV; ++v) in_range = in_range && finite(A[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) in_range = in_range && finite(S[v]);
+    if (__any_sync(0xffffffffu, !in_range && in_c)) {
+#pragma unroll
+      for (int v = 0; v < GV; ++v) A[v] = 1.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) S[v] = 0.f;
+      start<false>(a);
+      stream<false>(a, [&](auto, int, const B& r) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          float xf[V], gf[GV];
+          r.x[i].widen(xf);
+          r.g[i].widen(gf);
+          advance(S, gf, xf);
+#pragma unroll
+          for (int v = 0; v < GV; ++v) A[v] = gate_product(A[v], gf[v]);
+        }
+      });
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) pair[v] = make_float2(A[kHead ? 0 : v], S[v]);
   }
@@ -476,7 +509,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 #pragma unroll 4
     for (int w = 1; w < p.parts; ++w) {
       const float2 m = s_pair[w * wide + k];
-      n = make_float2(n.x * m.x, past(m, n.y));
+      n = make_float2(gate_product(n.x, m.x), past(m, n.y));
     }
     a.chunks[row * width + p.group * wide + k] = n;
   }
@@ -546,7 +579,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
       float2 n[V];
       load_pairs(src, n);
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum[v] = make_float2(sum[v].x * n[v].x, past(n[v], sum[v].y));
+      for (int v = 0; v < V; ++v) sum[v] = make_float2(gate_product(sum[v].x, n[v].x), past(n[v], sum[v].y));
     }
     store_pairs(s_pair + p.part * wide + p.k, sum);
     store_pairs(s_slice + p.part * wide + p.k, own);

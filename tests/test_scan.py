@@ -360,3 +360,68 @@ def test_c_entry_refuses_without_a_gpu():
         assert lib.arl2_scan_backward(f, None) == bad
     f = arl2._SCAN_BWD.pack(*sh, p, p, p, 0, 0, p, p, 0, 0, *s2, *s3, *s2, 512, 0)
     assert lib.arl2_scan_backward(f, None) == bad
+
+
+# ------------------------------------------------------------------------- gates above 1
+def against_loop(x, dh, a, h0, dfinal, heads, dtype, gate, lens=None):
+    """Both directions on given inputs, compared as check() does."""
+    B, T, C = x.shape
+    n = [T] * B if lens is None else lens
+    dev = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    z = lambda t: np.zeros((B, C)) if t is None else t.double().cpu().numpy()
+    X, A, D = x.double().cpu().numpy(), channels(a, heads, C), dh.double().cpu().numpy()
+    depth = 2 * T + 80
+    h, final = arl2.scan_forward(x, a, h0=h0, lens=dev)
+    rh, rf = loop_forward(X, A, z(h0), n)
+    sh, sf = loop_forward(np.abs(X), np.abs(A), np.abs(z(h0)), n)
+    close(h, rh, sh, depth, DT[dtype])
+    close(final, rf, sf, depth, torch.float32)
+    dx, da, dh0 = arl2.scan_backward(dh, a, h, h0=h0, dfinal=dfinal, lens=dev)
+    H = h.double().cpu().numpy()
+    rdx, rda, rdh0 = loop_backward(D, A, H, z(h0), z(dfinal), n)
+    sdx, sda, sdh0 = loop_backward(np.abs(D), np.abs(A), np.abs(H), np.abs(z(h0)), np.abs(z(dfinal)), n)
+    close(dx, rdx, sdx, depth, DT[dtype])
+    close(dh0, rdh0, sdh0, depth + 1, torch.float32)
+    if heads:
+        fold = lambda v: v.reshape(B, T, heads, C // heads).sum(axis=3).transpose(0, 2, 1)
+        close(da, fold(rda), fold(sda), depth + 1 + C // heads, torch.float32)
+    else:
+        close(da, rda, sda, depth + 1, DT[gate])
+
+
+@on_gpu
+@pytest.mark.parametrize("T", [40, 400, 1000, 2500, 4100])
+@pytest.mark.parametrize("C,heads,dtype,gate", [(128, 0, "bf16", "bf16"), (37, 0, "fp32", "fp32"),
+                                                (64, 2, "fp32", "fp32")])
+def test_a_state_of_zero_stays_zero_under_gates_above_one(T, C, heads, dtype, gate):
+    # The gates' product over the part without input passes fp32's range many times; the states do
+    # not: 0 there, then values under gates below 1. Before them one gate of 0, which forgets.
+    B, n = 2, 30
+    r = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=r, device="cuda")
+    for part in ("forward", "backward"):
+        x, dh = rand(B, T, C).to(DT[dtype]), rand(B, T, C).to(DT[dtype])
+        a = torch.sigmoid(rand(B, heads, T) if heads else rand(B, T, C))
+        at = (lambda s: a[:, :, s]) if heads else (lambda s: a[:, s])
+        if part == "forward":     # no gradient reaches the tokens under large gates
+            x[:, :T - n] = 0
+            at(slice(0, T - n))[:] = -16.0
+            at(T - n - 1)[:] = 0.0
+            dh[:, :T - n] = 0
+        else:                     # dh = 0 behind the first n tokens, x = 0 as well, and the state forgotten
+            dh[:, n:] = 0
+            x[:, n:] = 0
+            at(slice(n, T))[:] = 16.0
+            at(n)[:] = 0.0
+        against_loop(x, dh, a.to(DT[gate]), None, None, heads, dtype, gate)
+
+
+@on_gpu
+def test_negative_gates_and_growth_within_range():
+    # Gates of either sign, products of up to 2^100 over a sequence.
+    B, T, C = 2, 1500, 36
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, dh = (torch.randn(B, T, C, generator=g, device="cuda") * 2.0 ** -60 for _ in range(2))
+    a = torch.where(torch.rand(B, T, C, generator=g, device="cuda") < 0.5, -1.0, 1.0) * 2.0 ** (100 / T)
+    h0, dfinal = (torch.randn(B, C, generator=g, device="cuda") * 2.0 ** -60 for _ in range(2))
+    against_loop(x, dh, a, h0, dfinal, 0, "fp32", "fp32")
