@@ -425,3 +425,23 @@ def test_negative_gates_and_growth_within_range():
     a = torch.where(torch.rand(B, T, C, generator=g, device="cuda") < 0.5, -1.0, 1.0) * 2.0 ** (100 / T)
     h0, dfinal = (torch.randn(B, C, generator=g, device="cuda") * 2.0 ** -60 for _ in range(2))
     against_loop(x, dh, a, h0, dfinal, 0, "fp32", "fp32")
+
+
+# ------------------------------------------------------------ lengths over several chunks
+@on_gpu
+@pytest.mark.parametrize("T", [2100, 4100])
+@pytest.mark.parametrize("C,heads,dtype,gate", [(256, 2, "bf16", "fp32"), (128, 0, "bf16", "bf16"),
+                                                (61, 0, "fp32", "fp32"), (72, 0, "fp16", "fp32")])
+@pytest.mark.parametrize("state", [True, False])
+def test_lengths_over_chunks(T, C, heads, dtype, gate, state):
+    # Empty, one token, on and next to the edges of slices and chunks (multiples of 8), one short of
+    # full; NaN behind each.
+    check(8, T, C, heads, dtype, gate, seed=T, lens=[T, 0, 1, 512, 513, 1024, 1031, T - 1], state=state)
+
+
+@on_gpu
+@pytest.mark.parametrize("C,heads,dtype", [(520, 0, "bf16"), (384, 3, "bf16")])
+def test_long_slices_of_one_chunk(C, heads, dtype):
+    # More (sequence, channel group) pairs than the GPU takes at once: one chunk, slices of over 64 tokens.
+    B, T = 150, 1100
+    check(B, T, C, heads, dtype, "fp32", lens=[T - 7 * b for b in range(B)])
