@@ -313,8 +313,10 @@ void arl2_kvcache_destroy(arl2_kvcache* c);
  * elements must not share memory, and outputs must not overlap inputs. lse: fp32
  * [B, H, Tq] contiguous. q_len, k_len: int32 [B] in device memory (clamped to [0, Tq], [0, Tk]),
  * or NULL for full lengths. scale: finite and positive, or 0 for 1 / sqrt(d).
- * P and dS are rounded to the type for the tensor cores; statistics, sums and gradients are
- * fp32 until they are stored, rounded once. Results do not depend on timing. */
+ * P and dS are rounded to the type for the tensor cores, in fp16 times powers of two found from
+ * the sizes of do and v in each call, which keep them in its range: the gradients have fp16's
+ * precision whatever the size of do is. Statistics, sums and gradients are fp32 until they are
+ * stored, rounded once. Results do not depend on timing. */
 typedef struct arl2_attn arl2_attn; /* opaque; owned by the library */
 typedef struct {
   void* ptr;
@@ -340,7 +342,7 @@ typedef struct {
 
 /* Create a context for B sequences of H query and H_kv key heads, up to max_Tq queries and
  * max_Tk keys (at most 2^28), on the current device. It allocates the scratch of both calls
- * (about 60 MB at d = 128, plus 8 bytes per query row and head) and no call allocates more.
+ * (about 60 MB at d = 128, plus 8 bytes per query row and head, 12 in fp16) and no call allocates more.
  * Calls with smaller Tq and Tk are served by the same context. The device must be current in
  * every call. Calls on one context, replays of captured ones included, share its scratch: they
  * must be ordered, normally by one stream. */

@@ -16,6 +16,7 @@ struct arl2_attn {
   float* records = nullptr;        // partial records of shared tiles, two per CTA
   float* dq_records = nullptr;     // the dq kernel's
   float* stats = nullptr;          // backward: row statistics
+  unsigned long long* range = nullptr;   // backward, fp16: the words of arl2::GradRange, call first
   void* splits = nullptr;          // the CTAs' splits, where a launch of its own makes them
   unsigned int* err = nullptr;     // the error word, then the backward kernel's two tickets
   unsigned long long timeout_ns = 1000000000ull;
@@ -109,6 +110,11 @@ arl2::AttnOut out_of(const arl2_tensor* t) {
   return {static_cast<uint16_t*>(t->ptr), t->stride[0], t->stride[1], t->stride[2]};
 }
 
+arl2::GradRange range_of(const arl2_attn* c) {
+  if (!c->range) return {};
+  return {c->range, c->range + 1, c->range + 1 + static_cast<size_t>(c->B) * c->Hkv * tiles(c->max_Tq, 128)};
+}
+
 arl2::AttnArgs args_of(const arl2_attn* c, const arl2_attn_shape* s) {
   arl2::AttnArgs a{};
   a.mask = {s->q_len, s->k_len, s->Tq, s->Tk, s->frame_len, s->q_start};
@@ -117,6 +123,7 @@ arl2::AttnArgs args_of(const arl2_attn* c, const arl2_attn_shape* s) {
   a.Hkv = c->Hkv;
   a.scale = s->scale > 0.f ? s->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c->d)));
   a.stats = c->stats;
+  a.range = range_of(c);
   a.records = c->records;
   a.dq_records = c->dq_records;
   a.splits = (s->q_len || s->k_len) && c->B > arl2::kSplitBatches ? c->splits : nullptr;
@@ -158,11 +165,15 @@ arl2_status arl2_attn_create(int B, int H, int H_kv, int max_Tq, int max_Tk, int
   c->half = dtype == ARL2_FP16;
   c->device = dev, c->sms = sms;
   const size_t bh = static_cast<size_t>(B) * H;
+  const size_t words = c->half ? 1 + static_cast<size_t>(B) * H_kv * (tiles(max_Tq, 128) + 1) : 0;
   const bool ok = alloc(&c->records, 2 * static_cast<size_t>(sms) * arl2::attn_record_floats(d), &c->bytes) &&
                   alloc(&c->dq_records, 2 * static_cast<size_t>(sms) * arl2::attn_dq_record_floats(d), &c->bytes) &&
                   alloc(reinterpret_cast<arl2::Split**>(&c->splits), sms, &c->bytes) &&
-                  alloc(&c->stats, bh * 2 * tiles(max_Tq, 128) * 128, &c->bytes) && alloc(&c->err, 3, &c->bytes) &&
-                  cudaMemset(c->err, 0, sizeof(unsigned int)) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+                  alloc(&c->stats, bh * arl2::attn_stat_rows(c->half) * tiles(max_Tq, 128) * 128, &c->bytes) &&
+                  alloc(&c->err, 3, &c->bytes) && cudaMemset(c->err, 0, sizeof(unsigned int)) == cudaSuccess &&
+                  (!words || (alloc(&c->range, words, &c->bytes) &&
+                              cudaMemset(c->range, 0, words * sizeof(*c->range)) == cudaSuccess)) &&
+                  cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     arl2_attn_destroy(c);
     return ARL2_ERR_OOM;
@@ -222,6 +233,11 @@ arl2_status arl2_attn_backward(arl2_attn* c, const arl2_attn_bwd* f, arl2_stream
   p.q_len = s->q_len;
   p.tickets = c->err + 1;
   p.B = c->B, p.H = c->H, p.Tq = s->Tq, p.d = c->d;
+  p.v = static_cast<const uint16_t*>(f->v.ptr);
+  p.v_sb = f->v.stride[0], p.v_st = f->v.stride[1], p.v_sh = f->v.stride[2];
+  p.k_len = s->k_len;
+  p.range = range_of(c);
+  p.Hkv = c->Hkv, p.Tk = s->Tk;
   arl2::AttnArgs a = args_of(c, s);
   a.o = out_of(&f->dq);
   a.dk = out_of(&f->dk);
@@ -249,6 +265,7 @@ void arl2_attn_destroy(arl2_attn* c) {
   cudaFree(c->records);
   cudaFree(c->dq_records);
   cudaFree(c->stats);
+  cudaFree(c->range);
   cudaFree(c->splits);
   cudaFree(c->err);
   delete c;

@@ -22,7 +22,8 @@
 // Roles (384 threads, one CTA per SM): warp 0 copies, warp 1 issues every MMA, warps 4-11 turn
 // scores into P and dS: thread = TMEM lane = row of the tile, warps 4-7 columns 0-63, 8-11 columns
 // 64-127, each in two packed halves (32 columns in place of 64 fp32 ones, at columns 0 and 64).
-// P and dS are rounded to 16 bits for the tensor cores; sums, statistics and gradients are fp32.
+// P and dS are rounded to 16 bits for the tensor cores, in fp16 times powers of two that keep them in
+// its range (GradRange); sums, statistics and gradients are fp32.
 #include <algorithm>
 
 #include "arl2_attn_kernels.h"
@@ -54,11 +55,33 @@ __device__ __forceinline__ void store32(uint16_t* dst, const float (&x)[32]) {
                    pack2<kHalf>(x[c + 6], x[c + 7]));
 }
 
-// Write kCols accumulator columns of this thread's row: to the output, times scale, when the
-// segment is the whole tile, otherwise to this group's place in a record, [kCols / 4][128] float4.
+// fp16's powers of two (GradRange).
+constexpr int kPShift = 14;   // P <= 1 becomes at most 2^14: a factor of 4 below the type's end
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int range_field(const unsigned long long* w) { return static_cast<int>(__ldcg(w) & 0x1ff); }
+// The e of 2^e dS <= 2^14 from the exponent fields of |do|^2 < 2^(x + 1) and |v|^2 < 2^(y + 1): |do| |v| is
+// below 2^ceil((x + y + 2) / 2), |dP - delta| below twice that. x and y of finite fp16 rows are in
+// [-48, 39] (or the field is that of 0).
+__device__ __forceinline__ int ds_exponent(int g_field, int v_field) {
+  const int x = min(max(g_field - 127, -48), 40), y = min(max(v_field - 127, -48), 40);
+  return 13 - ((x + y + 3) >> 1);
+}
+// That of a key tile (one warp): over the query tiles that see it.
+__device__ __forceinline__ int dk_exponent(const AttnArgs& a, int b, int h, int tile, int ql) {
+  const size_t bh = static_cast<size_t>(b) * a.Hkv + h;
+  const unsigned long long* g = a.range.g + bh * RowTiles<kRows>::count(a.mask);
+  int x = 0;
+  for (int i = KeyTiles::first_tile(a.mask, tile) + (threadIdx.x & 31); i * kRows < ql; i += 32)
+    x = max(x, range_field(g + i));
+  return ds_exponent(__reduce_max_sync(0xffffffffu, x), range_field(a.range.v + bh));
+}
+
+// Write kCols accumulator columns of this thread's row: to the output, times scale (fp16: and unscale,
+// for which the product of both might leave fp32's range), when the segment is the whole tile, otherwise
+// to this group's place in a record, [kCols / 4][128] float4.
 template <int kCols, bool kHalf>
 __device__ __forceinline__ void write_rows(const Seg& sg, uint32_t acc, int r, bool inside, bool zero, uint16_t* dst,
-                                           float scale, float* rec, uint32_t empty_bar) {
+                                           float scale, float unscale, float* rec, uint32_t empty_bar) {
 #pragma unroll 1
   for (int k = 0; k < kCols; k += 32) {
     uint32_t x[32];
@@ -66,7 +89,8 @@ __device__ __forceinline__ void write_rows(const Seg& sg, uint32_t acc, int r, b
     if (sg.whole) {
       float y[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) y[e] = zero ? 0.f : __uint_as_float(x[e]) * scale;
+      for (int e = 0; e < 32; ++e)
+        y[e] = zero ? 0.f : (kHalf ? __uint_as_float(x[e]) * unscale : __uint_as_float(x[e])) * scale;
       if (inside) store32<kHalf>(dst + k, y);
     } else {
       float4* ro = reinterpret_cast<float4*>(rec);
@@ -101,20 +125,90 @@ __device__ __forceinline__ void add_records(Rec&& record, int c0, int c1, int q0
 }
 
 // ------------------------------------------------------------------ prep
+__device__ __forceinline__ float row_sum(float s, int lanes, unsigned mask) {
+  for (int m = lanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(mask, s, m);
+  return s;
+}
+// fp16: the sum of the squares of 8 values, and by all 256 threads: a word of GradRange raised to the
+// largest exponent field among them. With 18720 rows each of do and v the launch takes 10.8 us, 6.5 without
+// the ranges; with an atomic per row instead of one per block it took 24.
+__device__ __forceinline__ float sum_squares(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float n = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    n = fmaf(x.x, x.x, n);
+    n = fmaf(x.y, x.y, n);
+  }
+  return n;
+}
+struct RangeWord {
+  unsigned long long* word;
+  unsigned long long call, now;
+  __device__ void start(unsigned long long* w, const unsigned long long* c) {
+    word = w;
+    if (threadIdx.x == 0) call = __ldcg(c), now = __ldcg(w);
+  }
+  __device__ void raise(int field) const {
+    __shared__ int top[8];
+    field = __reduce_max_sync(0xffffffffu, field);
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = field;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < 8; ++i) field = max(field, top[i]);
+    const unsigned long long w = (call << 9) + field;
+    if (now < w) atomicMax(word, w);
+  }
+};
+constexpr int kPrepVRows = 4;
+
 template <bool kHalf>
-__global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_constant__ AttnPrepArgs a) {
+__global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_constant__ AttnPrepArgs a, int v_blocks) {
   griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < 2) a.tickets[threadIdx.x] = 0;
   const int lanes = a.d / 8;                        // lanes per row, 16 bytes each
   const int Tpad = (a.Tq + kRows - 1) / kRows * kRows;
-  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / lanes;   // (b, t, h), h fastest
-  const int part = threadIdx.x % lanes;
-  if (row >= static_cast<long long>(a.B) * Tpad * a.H) return;   // whole rows leave together
-  const int h = static_cast<int>(row % a.H);
-  const long long bt = row / a.H;
-  const int t = static_cast<int>(bt % Tpad), b = static_cast<int>(bt / Tpad);
+  const int part = threadIdx.x % lanes, lane = threadIdx.x & 31;
+  const unsigned mask = ((1u << lanes) - 1) << (lane / lanes * lanes);   // the row's lanes
+  int b, t, h;
+  RangeWord word{};
+  if constexpr (kHalf) {
+    const int block = static_cast<int>(blockIdx.x);
+    if (block < v_blocks) {   // v: kPrepVRows rows of a thread's place each, of one head
+      const int step = 256 / lanes, chunks = (a.Tk + kPrepVRows * step - 1) / (kPrepVRows * step);
+      h = block / chunks % a.Hkv;
+      b = block / chunks / a.Hkv;
+      t = block % chunks * kPrepVRows * step + threadIdx.x / lanes;
+      word.start(a.range.v + static_cast<size_t>(b) * a.Hkv + h, a.range.call);
+      const int kl = a.k_len ? min(max(a.k_len[b], 0), a.Tk) : a.Tk;
+      const uint16_t* src = a.v + b * a.v_sb + h * a.v_sh + part * 8;
+      float n = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPrepVRows; ++i) {
+        const int ti = t + i * step;
+        const float ni = ti < kl ? sum_squares(*reinterpret_cast<const uint4*>(src + ti * a.v_st)) : 0.f;
+        n = fmax_nan(n, row_sum(ni, lanes, mask));
+      }
+      word.raise((__float_as_int(n) >> 23) & 0xff);
+      return;
+    }
+    // The others: a block's 256 / lanes rows (which divide 128) share a tile of 128 rows and a head.
+    const int in_tile = lanes / 2, bth = (block - v_blocks) / in_tile, bt = bth / a.H;
+    h = bth % a.H;
+    b = bt / (Tpad / kRows);
+    t = bt % (Tpad / kRows) * kRows + (block - v_blocks) % in_tile * (256 / lanes) + threadIdx.x / lanes;
+    word.start(a.range.g + (static_cast<size_t>(b) * a.Hkv + h / (a.H / a.Hkv)) * (Tpad / kRows) + t / kRows,
+               a.range.call);
+  } else {
+    const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / lanes, bt = row / a.H;
+    if (row >= static_cast<long long>(a.B) * Tpad * a.H) return;   // whole rows leave together
+    h = static_cast<int>(row % a.H);   // fastest
+    t = static_cast<int>(bt % Tpad), b = static_cast<int>(bt / Tpad);
+  }
   const int ql = a.q_len ? min(max(a.q_len[b], 0), a.Tq) : a.Tq;
   float s = 0.f, l = -INFINITY;   // both negated: the consumers add them
+  [[maybe_unused]] float n = 0.f;
   if (t < ql) {
     const uint4 ov = *reinterpret_cast<const uint4*>(a.o + b * a.o_sb + t * a.o_st + h * a.o_sh + part * 8);
     const uint4 gv = *reinterpret_cast<const uint4*>(a.g + b * a.g_sb + t * a.g_st + h * a.g_sh + part * 8);
@@ -133,16 +227,18 @@ __global__ void __launch_bounds__(256) arl2_attn_prep_kernel(const __grid_consta
       s = fmaf(x.y, y.y, s);
     }
     const float lse = a.lse[(static_cast<size_t>(b) * a.H + h) * a.Tq + t];
-    l = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
+    l = lse == -INFINITY ? -INFINITY : fmaf(lse, -1.4426950408889634f, kHalf ? kPShift : 0);
+    if constexpr (kHalf) n = sum_squares(gv);
   }
-  const int lane = threadIdx.x & 31;
-  const unsigned mask = ((1u << lanes) - 1) << (lane / lanes * lanes);   // the row's lanes
-  for (int m = lanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(mask, s, m);
+  s = row_sum(s, lanes, mask);
+  const int field = kHalf ? (__float_as_int(row_sum(n, lanes, mask)) >> 23) & 0xff : 0;
   if (part == 0) {
-    float* out = a.stats + (static_cast<size_t>(b) * a.H + h) * 2 * Tpad + t;
+    float* out = a.stats + (static_cast<size_t>(b) * a.H + h) * attn_stat_rows(kHalf) * Tpad + t;
     out[0] = l;
     out[Tpad] = -s;
+    if constexpr (kHalf) out[2 * Tpad] = static_cast<float>(field);
   }
+  if constexpr (kHalf) word.raise(field);
 }
 
 // ------------------------------------------------------------------ dk, dv
@@ -244,7 +340,8 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
           waited = true;
         }
         if (lead) {
-          const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + hd) * 2 * Tpad + i * kRows;
+          const float* st =
+              a.stats + (static_cast<size_t>(sg.b) * a.H + hd) * attn_stat_rows(kHalf) * Tpad + i * kRows;
           mbar_expect_tx(bar(kKTFull + nt % 2), 1024);
           bulk_load(t_ring + nt % 2 * 1024, st, 512, bar(kKTFull + nt % 2));
           bulk_load(t_ring + nt % 2 * 1024 + 512, st + Tpad, 512, bar(kKTFull + nt % 2));
@@ -371,6 +468,8 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
       }
       const int per_head = sg.units / group, first = KeyTiles::first_tile(a.mask, sg.tile);
       const int row0 = first_row(a.mask, j);   // the first query row that sees this key
+      const int e = kHalf ? dk_exponent(a, sg.b, sg.h, sg.tile, sg.ql) : 0;
+      [[maybe_unused]] const float2 to_ds = make_float2(pow2(e - kPShift), pow2(e - kPShift));
       int i = first + sg.kb % per_head;
       for (int u = sg.kb; u < sg.ke; ++u, ++n) {
         ok = mbar_wait_warp(bar(kKTFull + n % 2), (n / 2) & 1, g);
@@ -417,6 +516,10 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar(kKPReady));
+        if constexpr (kHalf) {   // from 2^14 P to 2^e P, while dP is under way
+#pragma unroll
+          for (int k = 0; k < 32; ++k) p[k] = __fmul2_rn(p[k], to_ds);
+        }
         ok = mbar_wait_warp(bar(kKDFull), n & 1, g);
         if (!ok) break;
         tc_fence_after();
@@ -425,13 +528,13 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
           tmem_ld32x2_wait(dp_col, d[0], dp_col + 32, d[1]);
 #pragma unroll
           for (int k = 0; k < 64; k += 4) {
-            const float4 e = st[32 + k / 4];
+            const float4 dl = st[32 + k / 4];
             const uint32_t* x = &d[k >> 5][k & 31];
             const float2 d0 = __fmul2_rn(
-                p[k / 2], __fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(e.x, e.y)));
+                p[k / 2], __fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(dl.x, dl.y)));
             const float2 d1 = __fmul2_rn(
                 p[k / 2 + 1],
-                __fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(e.z, e.w)));
+                __fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(dl.z, dl.w)));
             w[k / 2] = pack2<kHalf>(d0.x, d0.y);
             w[k / 2 + 1] = pack2<kHalf>(d1.x, d1.y);
           }
@@ -448,8 +551,8 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
       ++ns;
       tc_fence_after();
       float* rec = a.records + record_slot(sp, cta, sg.first) * attn_record_floats(D) + wg * D * kRows;
-      write_rows<D, kHalf>(sg, (wg ? c_dk : c_dv) + lanes, r, inside, j >= sg.kl, dst, wg ? a.scale : 1.f, rec,
-                           bar(kKAccEmpty));
+      write_rows<D, kHalf>(sg, (wg ? c_dk : c_dv) + lanes, r, inside, j >= sg.kl, dst, wg ? a.scale : 1.f,
+                           pow2(wg ? -e : -kPShift), rec, bar(kKAccEmpty));
     }
     __syncwarp();
     tc_fence_before();
@@ -656,8 +759,15 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMa
           if (inside && writes) store32<kHalf>(dst + k, z);
         continue;
       }
-      const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + sg.h) * 2 * Tpad + row;
-      const float2 neg_lse = make_float2(st[0], st[0]), neg_delta = make_float2(st[Tpad], st[Tpad]);
+      const float* st = a.stats + (static_cast<size_t>(sg.b) * a.H + sg.h) * attn_stat_rows(kHalf) * Tpad + row;
+      int e = 0;
+      float bias = st[0];
+      if constexpr (kHalf) {   // 2^e P straight away
+        e = ds_exponent(static_cast<int>(st[2 * Tpad]),
+                        range_field(a.range.v + static_cast<size_t>(sg.b) * a.Hkv + sg.h / group));
+        bias += e - kPShift;
+      }
+      const float2 neg_lse = make_float2(bias, bias), neg_delta = make_float2(st[Tpad], st[Tpad]);
       // Rows behind the length are not written; they count as seeing all, so that they do not make
       // every tile a masked one.
       const int limit = row < sg.ql ? key_limit(a.mask, row, sg.kl) : sg.kl;
@@ -708,7 +818,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMa
       tc_fence_after();
       float* rec = a.dq_records + record_slot(sp, cta, sg.first) * attn_dq_record_floats(D) + wg * kCols * kRows;
       if (writes)
-        write_rows<kCols, kHalf>(sg, c_dq + lanes + kCols * wg, r, inside, row >= sg.ql, dst, a.scale, rec,
+        write_rows<kCols, kHalf>(sg, c_dq + lanes + kCols * wg, r, inside, row >= sg.ql, dst, a.scale, pow2(-e), rec,
                                  bar(kQAccEmpty));
       else
         warp_arrive(bar(kQAccEmpty));
@@ -751,6 +861,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       kind ^= 1;
       c = static_cast<int>(atomicAdd(a.tickets + kind, 1u));
     }
+    // The one CTA with dk's first range counts the call: the next prep, which is the next to read it,
+    // starts after this grid.
+    if (kHalf && kind == 0 && c == 0) ++*a.range.call;
     ticket[0] = kind;
     ticket[1] = c;
   }
@@ -800,8 +913,21 @@ __global__ void __launch_bounds__(kRows, 4)
                 k0 / 4, r, y);
   const bool zero = row >= (what < 2 ? kl : ql);
   const float scale = what == 0 ? 1.f : a.scale;
+  if constexpr (kHalf) {
+    int e = kPShift;   // as the kernel that wrote the records
+    if (what == 1) {
+      e = dk_exponent(a, sp.b, sp.h, sp.tile, ql);
+    } else if (what == 2) {
+      const int Tpad = RowTiles<kRows>::count(a.mask) * kRows;
+      e = ds_exponent(
+          static_cast<int>(a.stats[((static_cast<size_t>(sp.b) * a.H + sp.h) * attn_stat_rows(kHalf) + 2) * Tpad + row]),
+          range_field(a.range.v + static_cast<size_t>(sp.b) * a.Hkv + sp.h / group));
+    }
 #pragma unroll
-  for (int e = 0; e < 32; ++e) y[e] = zero ? 0.f : y[e] * scale;
+    for (int k = 0; k < 32; ++k) y[k] *= pow2(-e);
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k) y[k] = zero ? 0.f : y[k] * scale;
   const AttnOut& out = what == 0 ? a.dv : what == 1 ? a.dk : a.o;
   if (row < (what < 2 ? a.mask.Tk : a.mask.Tq))
     store32<kHalf>(out.ptr + sp.b * out.sb + row * out.st + sp.h * out.sh + k0, y);
@@ -832,11 +958,14 @@ template <int D, bool kHalf>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& g,
                    const AttnPrepArgs& prep, const AttnArgs& a, int ctas, bool combine, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.B) * ((a.mask.Tq + kRows - 1) / kRows * kRows) * a.H;
-  const unsigned blocks = static_cast<unsigned>((rows * (D / 8) + 255) / 256);
+  const int v_rows = kPrepVRows * 256 / (D / 8);   // of a block
+  const long long v_blocks = kHalf ? static_cast<long long>(a.B) * a.Hkv * ((a.mask.Tk + v_rows - 1) / v_rows) : 0;
+  const unsigned blocks = static_cast<unsigned>((rows * (D / 8) + 255) / 256 + v_blocks);
   const int n_dkv = attn_dkv_ctas(ctas), n_dq = ctas - n_dkv;
   cudaError_t e = cudaSuccess;
   if (a.splits) e = launch_chained(arl2_attn_bwd_split_kernel, dim3(ctas), 32, 0, st, false, a, n_dkv);
-  if (e == cudaSuccess) e = launch_chained(arl2_attn_prep_kernel<kHalf>, dim3(blocks), 256, 0, st, false, prep);
+  if (e == cudaSuccess) e = launch_chained(arl2_attn_prep_kernel<kHalf>, dim3(blocks), 256, 0, st, false, prep,
+                                            static_cast<int>(v_blocks));
   if (e == cudaSuccess)
     e = launch_chained(arl2_attn_bwd_kernel<D, kHalf>, dim3(ctas), kBwdThreads, bwd_smem<D>(), st, true, q, k, v, g, a,
                        n_dkv);

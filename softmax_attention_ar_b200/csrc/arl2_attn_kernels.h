@@ -15,6 +15,20 @@ struct AttnOut {          // an output tensor [B, T, heads, d], strides in eleme
   long long sb, st, sh;
 };
 
+// fp16 holds normal values from 2^-14 to 2^16 only, and P (about 1 / Tk) and dS (P times a gradient)
+// leave that range where the gradients themselves do not. So the backward pass carries 2^14 P, and 2^e dS
+// with e from a bound (Cauchy-Schwarz) of |dP - delta| <= 2 |do_i| |v_j|: e follows the row in dq, where a
+// row's sum is over keys, and the rows that see a key tile in dk. Both are undone in fp32, by powers of
+// two. The largest |do|^2 of a query tile and |v|^2 of a key head are found by prep as words of
+// (call << 9) + exponent field, so that what an earlier call left is below any of this call's.
+struct GradRange {
+  unsigned long long* call;   // counts the calls; the main kernel of a call adds 1
+  unsigned long long* g;      // [B][Hkv][query tiles]: over the query heads of the group
+  unsigned long long* v;      // [B][Hkv]
+};
+// Rows of statistics: -lse in log2 units (fp16: + 14), -delta; fp16: the exponent field of |do|^2.
+__host__ __device__ constexpr int attn_stat_rows(bool half) { return half ? 3 : 2; }
+
 struct AttnArgs {
   AttnMask mask;
   int B, H, Hkv;
@@ -22,7 +36,8 @@ struct AttnArgs {
   AttnOut o;              // forward: o; backward: dq
   AttnOut dk, dv;         // backward
   float* lse;             // forward: [B, H, Tq] out
-  const float* stats;     // backward: [B H][2][Tq rounded up to 128]: -lse in log2 units, then -delta
+  const float* stats;     // backward: [B H][kStatRows][Tq rounded up to 128], see attn_stat_rows
+  GradRange range;        // backward, fp16
   float* records;         // partial records, two per CTA
   float* dq_records;      // the dq kernel's
   void* splits;           // the CTAs' splits, written by a launch of its own, or null: each computes its own
@@ -41,6 +56,12 @@ struct AttnPrepArgs {
   const int* q_len;
   unsigned int* tickets;  // zeroed
   int B, H, Tq, d;
+  // fp16: v and where its range and that of do go.
+  const uint16_t* v;
+  long long v_sb, v_st, v_sh;
+  const int* k_len;
+  GradRange range;
+  int Hkv, Tk;
 };
 
 // Forward, and dk with dv.

@@ -571,3 +571,113 @@ def test_rows_behind_the_last_query_reach_no_gradient(Tq, q_len, dtype):
     assert op.status() == arl2.ARL2_OK
     assert (dv[0, :, 0] == 0).all() and (dk[0, :, 0] == 0).all()
     assert all(torch.isfinite(t[0, :, 1]).all() for t in (o, dq, dk, dv))
+
+
+# ------------------------------------------------------------------- the range of fp16
+def norms_close(got, want, name):
+    """By norms, dtype fp16. On its way to a gradient a term is rounded to fp16 as P or dS, through o in
+    delta and with the stored sum: at most 2^-11 relative each. The terms have independent signs, and so
+    have their roundings: in norm 3 * 2^-11 of the gradient's. What fp16 cannot hold of the exact gradient
+    (values among its subnormals) comes on top; a value next to a rounding border may go to either side,
+    so twice."""
+    got, want = got.double(), want.double()
+    assert torch.isfinite(got).all(), name
+    off, held = (got - want).norm().item(), (want.to(HF).double() - want).norm().item()
+    assert off <= 3 * 2.0 ** -11 * want.norm().item() + 2 * held, f"{name}: {off:.3e} of {want.norm().item():.3e}"
+
+
+def half_gradients(q, k, v, do, op=None, **kw):
+    """The kernel's gradients of fp16 inputs and the fp64 ones, heads first."""
+    B, Tq, H, d = q.shape
+    op = op or arl2.SoftmaxAttention(H, Tq, k.shape[1], d, B=B, H_kv=k.shape[2], dtype=HF)
+    o, lse = op.forward(q, k, v, **kw)
+    got = op.backward(do, q, k, v, o, lse, **kw)
+    assert op.status() == arl2.ARL2_OK
+    m = visible(B, Tq, k.shape[1], None, None, kw.get("frame_len", 0), kw.get("q_start", 0))
+    r, _, _ = reference(q, k, v, do, m, d ** -0.5)
+    return [t.double().permute(0, 2, 1, 3) for t in got], [r[n] for n in ("dq", "dk", "dv")]
+
+
+@on_gpu
+@pytest.mark.parametrize("size", [1e-5, 1e-4, 1e-3, 1.0, 1e3])
+@pytest.mark.parametrize("Tq,Tk,H,Hkv,d", [(500, 12480, 2, 1, 128), (2100, 2100, 2, 2, 64)])
+def test_fp16_gradients_of_any_size(Tq, Tk, H, Hkv, d, size):
+    # Over long keys P and dS lie far below fp16's normal range, whatever do is.
+    q, k, v, do = make(1, Tq, Tk, H, Hkv, d, torch.float32, seed=14)
+    q, k, v, do = q.to(HF), k.to(HF), v.to(HF), (do * size).to(HF)
+    for name, got, want in zip(("dq", "dk", "dv"), *half_gradients(q, k, v, do)):
+        norms_close(got, want, name)
+
+
+@on_gpu
+@pytest.mark.parametrize("d", [32, 128])
+def test_fp16_scores_gradient_above_the_types_range(d):
+    # Two keys with opposite values, a large loss scale: dS is about 128000, the gradients are not.
+    g = torch.Generator().manual_seed(15)
+    r = lambda *s: torch.randn(*s, generator=g)
+    q, k = (0.1 * r(1, 8, 1, d)).to(HF).cuda(), (0.1 * r(1, 2, 1, d)).to(HF).cuda()
+    v = torch.ones(1, 2, 1, d, dtype=HF, device="cuda")
+    v[:, 1] = -1
+    do = (2000 * 128 / d * (1 + 0.1 * r(1, 8, 1, d))).to(HF).cuda()
+    for name, x, y in zip(("dq", "dk", "dv"), *half_gradients(q, k, v, do)):
+        norms_close(x, y, name)
+
+
+@on_gpu
+def test_fp16_rows_batches_heads_and_frames_of_different_size():
+    # Each keeps its own precision: rows for dq; sequences, key heads and the frames that see a key for dk.
+    B, T, H, Hkv, d, F = 2, 1024, 4, 2, 64, 256
+    q, k, v, do = make(B, T, T, H, Hkv, d, torch.float32, seed=16)
+    do[:, 1::2] *= 2.0 ** -12
+    do[1] *= 2.0 ** -4
+    do[:, :, 2:] *= 2.0 ** -3
+    q, k, v, do = q.to(HF), k.to(HF), v.to(HF), (do * 4096).to(HF)
+    (dq, dk, dv), (rq, rk, rv) = half_gradients(q, k, v, do, frame_len=F)
+    for b in range(B):
+        for h in range(H):
+            for odd in range(2):
+                norms_close(dq[b, h, odd::2], rq[b, h, odd::2], f"dq {b} {h} {odd}")
+        for h in range(Hkv):
+            norms_close(dk[b, h], rk[b, h], f"dk {b} {h}")
+            norms_close(dv[b, h], rv[b, h], f"dv {b} {h}")
+    # The last frame's gradients far smaller than the earlier ones': its keys are seen by it alone.
+    do[:, 768:] *= 2.0 ** -14
+    (dq, dk, dv), (rq, rk, rv) = half_gradients(q, k, v, do, frame_len=F)
+    for f in range(4):
+        s = slice(f * F, (f + 1) * F)
+        for name, x, y in (("dq", dq, rq), ("dk", dk, rk), ("dv", dv, rv)):
+            for b in range(B):
+                norms_close(x[b, :, s], y[b, :, s], f"{name} {b} frame {f}")
+
+
+@on_gpu
+def test_fp16_range_is_taken_anew_in_every_call():
+    # A call with large gradients before one with small ones, eager and replayed, with lengths that
+    # leave rows out: equal to a context that saw nothing before.
+    B, T, H, d = 2, 700, 2, 64
+    n = torch.tensor([700, 300], dtype=torch.int32, device="cuda")
+    q, k, v, base = make(B, T, T, H, H, d, HF, seed=17)
+    sizes = [2.0 ** e for e in (13, -10, 0, -14)]
+
+    def fresh(size):
+        op = arl2.SoftmaxAttention(H, T, T, d, B=B, dtype=HF)
+        o, lse = op.forward(q, k, v, q_len=n, k_len=n)
+        return op.backward(base * size, q, k, v, o, lse, q_len=n, k_len=n)
+
+    want = [fresh(s) for s in sizes]
+    op = arl2.SoftmaxAttention(H, T, T, d, B=B, dtype=HF)
+    o, lse = op.forward(q, k, v, q_len=n, k_len=n)
+    for s, w in zip(sizes, want):
+        got = op.backward(base * s, q, k, v, o, lse, q_len=n, k_len=n)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
+    do = base.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = op.backward(do, q, k, v, o, lse, q_len=n, k_len=n)
+    for s, w in zip(sizes, want):
+        do.copy_(base * s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
+    assert op.status() == arl2.ARL2_OK
