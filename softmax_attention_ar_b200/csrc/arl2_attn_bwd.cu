@@ -4,7 +4,8 @@
 // over the visible pairs (arl2_attn.cuh). lse comes from the forward call, so P needs no second
 // pass over the keys.
 //
-// The tensor cores bound it. Launches, each a programmatic dependent of the one before:
+// The tensor cores bound it. Launches, the second and the third each a programmatic dependent of the
+// one before (behind a split launch, arl2_attn.cuh, prep is an ordinary one):
 //   - arl2_attn_prep_kernel: -delta, and -lse in log2 units (-inf where a row sees nothing or lies
 //     behind its length: P is then 0), padded to whole 128-row tiles;
 //   - arl2_attn_bwd_kernel, some of whose CTAs compute dk and dv (dkv_cta): a tile is 128 keys of
@@ -313,7 +314,7 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
     const bool lead = elect_one();
     const int Tpad = (a.mask.Tq + kRows - 1) / kRows * kRows;
     uint32_t ns = 0, nq = 0, ng = 0, nt = 0, side_phase = 0;   // copies made
-    bool ok = true, waited = false;
+    bool ok = true;
     while (ok && walk.next(sg)) {
       if (sg.units == 0) continue;
       if (ns > 0 && !mbar_wait_warp(bar(kKKVEmpty), (ns - 1) & 1, g)) break;
@@ -335,10 +336,6 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
         if (!ok) break;
         ok = nt < 2 || mbar_wait_warp(bar(kKTEmpty + nt % 2), (nt / 2 - 1) & 1, g);
         if (!ok) break;
-        if (!waited) {   // the statistics come from the launch before this one
-          griddep_wait();
-          waited = true;
-        }
         if (lead) {
           const float* st =
               a.stats + (static_cast<size_t>(sg.b) * a.H + hd) * attn_stat_rows(kHalf) * Tpad + i * kRows;
@@ -360,7 +357,6 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_q, const CUtensorM
       }
     }
     __syncwarp();
-    if (!waited) griddep_wait();   // this grid ends after the one before it
     // Every copy issued lands before the CTA may exit.
     if (ns > 0) mbar_wait_drain(bar(kKKVFull), (ns - 1) & 1);
     for (uint32_t s = 0; s < 3; ++s)
@@ -748,7 +744,6 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_q, const CUtensorMa
     const bool writes = D > 32 || wg == 0;
     uint32_t n = 0, ns = 0;
     bool ok = true;
-    griddep_wait();   // the statistics come from the launch before this one
     while (ok && walk.next(sg)) {
       const int row = sg.tile * kRows + r;
       uint16_t* dst = a.o.ptr + sg.b * a.o.sb + row * a.o.st + sg.h * a.o.sh + kCols * wg;
@@ -852,7 +847,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int n_dq = static_cast<int>(gridDim.x) - n_dkv;
   int* ticket = reinterpret_cast<int*>(attn_smem);
   if (threadIdx.x == 0) {
-    griddep_wait();   // the launch before this one zeroed the tickets
+    griddep_wait();   // for all threads: the launch before this one zeroed the tickets and made the statistics
     uint32_t sm;
     asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
     int kind = static_cast<int>(sm & ~1u) < n_dkv ? 0 : 1;

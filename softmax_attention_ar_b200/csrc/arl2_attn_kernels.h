@@ -73,7 +73,8 @@ cudaError_t attn_bwd_setup();
 // same tile pairs to do, of 4 and 3 products: 2590 and 2230 cycles each as measured at d = 128.
 // An even number, for whole pairs of SMs.
 inline int attn_dkv_ctas(int ctas) { return ctas < 4 ? 1 : (ctas * 259 / (259 + 223) + 1) / 2 * 2; }
-// Each launches as a programmatic dependent of the one before it in the same call. combine: a
+// Within a call the backward kernel (behind prep) and the combining launches are programmatic dependents
+// of the launch before; a call's first launch, and what follows a split launch, are not. combine: a
 // tile may be shared between CTAs, so its records have to be added up.
 cudaError_t launch_attn_fwd(int d, bool half, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                             const AttnArgs& a, int ctas, bool combine, cudaStream_t st);
