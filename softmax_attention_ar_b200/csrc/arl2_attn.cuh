@@ -382,7 +382,7 @@ __device__ __forceinline__ float2 exp2_poly4(float2 x) {
   return __fmul2_rn(p, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
                                    __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
 }
-// Column pairs, of every 8, that take it; the others go to the MUFU unit.
+// Column pairs, of every 8, that take it in the backward pass; the others go to the MUFU unit.
 __host__ __device__ constexpr bool fma_pair(uint32_t pairs, int j) { return (pairs >> (j & 7)) & 1u; }
 __device__ __forceinline__ float2 exp2_pair(float2 x, bool on_fma) {
   return on_fma ? exp2_poly4(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));

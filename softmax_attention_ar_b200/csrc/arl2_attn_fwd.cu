@@ -2,7 +2,9 @@
 //     o = softmax(scale q k^T + mask) v,    lse_i = log sum_j exp(scale q_i.k_j)
 // over the visible keys (arl2_attn.cuh). The 4 d flops per visible pair on the tensor cores
 // bound it; the exponentials come next (16 a clock and SM on the MUFU unit: 1024 clocks for a
-// 128 x 128 tile whose two products take 1024 clocks on the tensor pipe at d = 128).
+// 128 x 128 tile whose two products take 1024 clocks on the tensor pipe at d = 128). All of them go
+// there: with 3 of 8 as polynomials on the FMA pipe, which the rest of the softmax loads, one 480p frame
+// took 36.6 us (35.0 without) and eight frames 486 (478).
 //
 // A tile is two 128-row query tiles of one head (256 rows), which share every K and V tile
 // that is loaded. While the softmax of one works on its scores, the tensor pipe does the
@@ -58,7 +60,6 @@ constexpr uint32_t fwd_smem() {
 }
 static_assert(fwd_smem<128>() <= 232448, "shared memory per CTA");
 constexpr float kRaise = 8.0f;    // log2 units
-constexpr uint32_t kFwdFmaPairs = 0xA4u;   // exponentials on the FMA pipe: pairs 2, 5, 7 of 8
 
 // Per record: [2 query tiles][d / 4 quads][128 rows] float4 of O, then [2][2][128] m and l.
 template <int D>
@@ -381,10 +382,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int q = 0; q < 4; ++q) {
           float2 e[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            e[k] = exp2_pair(
-                __ffma2_rn(make_float2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), sc, sh),
-                fma_pair(kFwdFmaPairs, k));
+          for (int k = 0; k < 16; ++k) {
+            const float2 x =
+                __ffma2_rn(make_float2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), sc, sh);
+            e[k] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          }
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
