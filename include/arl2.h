@@ -305,7 +305,8 @@ void arl2_kvcache_destroy(arl2_kvcache* c);
  * place of query 0 among the keys. A row that sees nothing has o = 0, lse = -inf and dq = 0 (so
  * has one whose scores are all -inf, but for dq); dk and dv are 0 where nothing sees the key.
  * Rows of q, o and do behind q_len, and of k and v behind k_len, may hold anything: they reach
- * no result, and the rows of o, dq, dk and dv there are 0, those of lse -inf.
+ * no result, and the rows of o, dq, dk and dv there are 0, those of lse -inf. What only the frames
+ * hide has to be finite: 0 times it is added.
  * q, o, do, dq: [B, Tq, H, d]; k, v, dk, dv: [B, Tk, H_kv, d], of the context's type (bf16 or
  * fp16), d in {32, 64, 128}, given as a pointer and strides in elements (batch, token, head),
  * elements of a head adjacent: pointers 16-byte aligned, strides positive multiples of 8 (any

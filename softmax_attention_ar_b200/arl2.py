@@ -85,8 +85,6 @@ _SCAN_BWD = struct.Struct(_SCAN_SHAPE + "9P9q")
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # arl2_dtype
 
-
-
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -528,7 +526,7 @@ def scan_forward(x, a, h0=None, lens=None, out=None, final=None, stream=None):
     and token, fp32 [B, heads, T] with C / heads in {32, 64, 128} (the layout of
     ``ARL2Layer.gates``). h0 fp32 [B, C], 0 if None. lens int32 [B]: behind lens[b] h is 0, and
     the final state is that of the last token inside. With T = 1 this is the serving step. out
-    may be x, final may be h0.
+    may be x, final may be h0. The outputs carry no autograd graph; scan_backward gives the gradients.
     """
     index, shape, st_a, fields = _scan_shape(x, a, lens, "x")
     B, T, C = shape
@@ -615,6 +613,10 @@ class SoftmaxAttention:
     with frame_len > 0, j < (floor((i + q_start) / frame_len) + 1) * frame_len: its own frame
     and the ones before it (frame_len = 1: causal), q_start being the place of query 0 among
     the keys. Rows that see nothing give o = 0, lse = -inf. scale defaults to 1 / sqrt(d).
+
+    Every call takes B sequences; a shorter batch is one whose last q_len and k_len are 0. The
+    outputs carry no autograd graph, whether or not the inputs require gradients: ``backward`` is
+    what a ``torch.autograd.Function`` around the two calls would use.
 
     The scratch belongs to the object: calls on one object, and replays of graphs that captured
     them, must be ordered, normally by one stream.

@@ -58,8 +58,8 @@ __device__ __forceinline__ int first_row(const AttnMask& m, int j) {
 template <int kRowsPerTile>
 struct RowTiles {
   // What cutting tiles costs, in units per CTA: records to write, the pipeline to fill again, and
-  // the launch that adds. Forward, one 480p frame of 12 heads: 84 tiles of 13 units take 37 us
-  // whole and 43 us cut into 148 ranges of 7.4 units. Backward, it hardly matters.
+  // the launch that adds. Forward, one 480p frame of 12 heads: 84 tiles of 13 units take 33 us
+  // whole and 39 us cut into 148 ranges of 7.4 units. Backward, it hardly matters.
   static constexpr int kCutCost = kRowsPerTile == kRows ? 2 : 8;
   static __device__ int count(const AttnMask& m) { return (m.Tq + kRowsPerTile - 1) / kRowsPerTile; }
   static __device__ int valid(const AttnMask& m, int ql, int) { return (ql + kRowsPerTile - 1) / kRowsPerTile; }
