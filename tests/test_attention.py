@@ -681,3 +681,22 @@ def test_fp16_range_is_taken_anew_in_every_call():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, w))
     assert op.status() == arl2.ARL2_OK
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_zero_and_infinite_gradients(dtype):
+    # All of do 0: gradients of exactly 0. An infinity in one head: the other head's stay as they are.
+    T, H, d = 300, 2, 64
+    q, k, v, do = make(1, T, T, H, H, d, dtype, seed=18)
+    op = arl2.SoftmaxAttention(H, T, T, d, dtype=dtype)
+    o, lse = op.forward(q, k, v)
+    assert all((t == 0).all() for t in op.backward(torch.zeros_like(do), q, k, v, o, lse))
+    want = op.backward(do, q, k, v, o, lse)
+    do[0, 77, 0, 5] = float("inf")
+    got = op.backward(do, q, k, v, o, lse)
+    assert op.status() == arl2.ARL2_OK
+    assert all(torch.equal(x[:, :, 1], y[:, :, 1]) for x, y in zip(got, want))
+    assert not torch.isfinite(got[2][0, :, 0, 5]).any()
+    rows = torch.arange(T, device="cuda") != 77
+    assert torch.isfinite(got[0][0, rows]).all()

@@ -445,3 +445,20 @@ def test_long_slices_of_one_chunk(C, heads, dtype):
     # More (sequence, channel group) pairs than the GPU takes at once: one chunk, slices of over 64 tokens.
     B, T = 150, 1100
     check(B, T, C, heads, dtype, "fp32", lens=[T - 7 * b for b in range(B)])
+
+
+@on_gpu
+def test_gates_above_one_with_lengths():
+    # As above, with sequences of different length, one of them empty.
+    B, T, C, n = 5, 2600, 72, 30
+    lens = [T, 0, 700, 1033, T - 1]
+    g = torch.Generator(device="cuda").manual_seed(19)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, dh, a = rand(B, T, C).bfloat16(), rand(B, T, C).bfloat16(), torch.full((B, T, C), -16.0, device="cuda")
+    for b, m in enumerate(lens):
+        m = max(m, n + 1)
+        x[b, :m - n] = 0
+        dh[b, :m - n] = 0
+        a[b, m - n - 1] = 0
+        a[b, m - n:m] = torch.sigmoid(rand(n, C))
+    against_loop(x, dh, a.bfloat16(), None, None, 0, "bf16", "bf16", lens=lens)
